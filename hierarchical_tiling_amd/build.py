@@ -39,6 +39,9 @@ SOURCES = [
     ("reduce.hip", HIP),
     ("probe.hip", HIP),
     ("repack.hip", HIP),
+    ("scaled.hip", HIP),
+    ("quant.hip", HIP),
+    ("route.hip", HIP),
     ("api.cpp", HIP),
     ("layout.cpp", ["g++"] + COMMON),
 ]
@@ -47,12 +50,18 @@ SOURCES = [
 HEADERS = [os.path.join(CSRC, "kernels.h"), os.path.join(CSRC, "pingpong.h"), os.path.join(CSRC, "gemm_internal.h"),
            os.path.join(CSRC, "atom_maps.h"),
            os.path.join(ROOT, "include", "htgemm.h"), os.path.join(ROOT, "include", "htlayout.h")]
+# headers that only some sources read, besides those
+OWN_HEADERS = {
+    "scaled.hip": [os.path.join(CSRC, "scaled.h"), os.path.join(ROOT, "include", "htscaled.h")],
+    "quant.hip": [os.path.join(ROOT, "include", "htscaled.h")],
+    "route.hip": [os.path.join(ROOT, "include", "htroute.h")],
+}
 
 
 def _compile(src, cmd, incremental=False):
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
     if incremental and os.path.exists(obj):
-        newest = max(os.path.getmtime(f) for f in HEADERS + [os.path.join(CSRC, src)])
+        newest = max(os.path.getmtime(f) for f in HEADERS + OWN_HEADERS.get(src, []) + [os.path.join(CSRC, src)])
         if os.path.getmtime(obj) > newest:
             return obj
     full = cmd + ["-c", os.path.join(CSRC, src), "-o", obj]

@@ -571,6 +571,23 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 }  // namespace
 
+// check_arch for calls that are made every step: the answer for a device is kept (its
+// architecture does not change), so only the first call on it queries the runtime.
+int htk::arch_status() {
+  constexpr int kSeen = 64;
+  static std::atomic<int> seen[kSeen];  // 0: not asked yet, else 1 + status
+  const char* fake = std::getenv("HTGEMM_FAKE_ARCH");
+  if (fake && *fake) return check_arch();
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess) return GEMM_ERR_HIP;
+  if (dev < 0 || dev >= kSeen) return check_arch();
+  const int known = seen[dev].load(std::memory_order_relaxed);
+  if (known) return known - 1;
+  const int rc = check_arch();
+  if (rc == GEMM_OK || rc == GEMM_ERR_ARCH) seen[dev].store(1 + rc, std::memory_order_relaxed);
+  return rc;
+}
+
 extern "C" {
 
 int gemm_create(const gemm_desc* desc, gemm_t* out) {

@@ -1,0 +1,301 @@
+// quant.hip -- block quantisation to e4m3 (quant_blocks of htscaled.h).
+//
+// For a block with largest magnitude top:  t = max(top, 448 * 2^-126), scale = t / 448,
+// q = e4m3(clamp(x * (448 / t))).  Both kernels read x once, keep the block in registers between
+// the maximum and the conversion, and are bound by memory.
+#include <algorithm>
+
+#include "../../include/htscaled.h"
+#include "kernels.h"
+
+namespace htk {
+namespace {
+
+struct QParams {
+  const void* x;
+  const int32_t* index;
+  u8* q;
+  u8* qt;
+  float* scale;
+  float* scale_t;
+  int64_t rows, cols, ldx, x_rows;
+  int64_t ldq, ldqt, q_cols, qt_cols;   // q_cols, qt_cols: written columns, zeros past the data
+  int64_t scale_r, scale_c, scale_t_c, scale_t_r;
+  int index_div, pow2, block;           // block: one scale for 128 x 128
+  int x_vec, q_vec, qt_vec;             // rows start on 16 (x, qt) and 8 (q) bytes
+};
+
+template <int XT> struct XType;
+template <> struct XType<DT_F32> {
+  typedef float T;
+  __device__ static float up(float v) { return v; }
+};
+template <> struct XType<DT_BF16> {
+  typedef u16 T;
+  __device__ static float up(u16 v) { return bf16_to_f32(v); }
+};
+template <> struct XType<DT_F16> {
+  typedef u16 T;
+  __device__ static float up(u16 v) { return f16_to_f32(v); }
+};
+
+// The source row of result row r, or -1 for a row of zeros.
+__device__ __forceinline__ int64_t source_row(const QParams& p, int64_t r) {
+  if (!p.index) return r;
+  const int i = p.index[r];
+  if (i < 0) return -1;
+  const int64_t s = p.index_div == 1 ? i : i / p.index_div;
+  return s < p.x_rows ? s : -1;
+}
+
+// Columns c .. c + 7 of source row s as fp32; zero past the row and for s < 0.
+template <int XT>
+__device__ __forceinline__ void load8(const QParams& p, int64_t s, int64_t c, float (&v)[8]) {
+  typedef typename XType<XT>::T T;
+  const T* src = (const T*)p.x + s * p.ldx + c;
+  if (s >= 0 && p.x_vec && c + 8 <= p.cols) {
+    constexpr int PER = 16 / (int)sizeof(T);
+    static_for<8 / PER>([&](auto h) {
+      const u32x4 w = reinterpret_cast<const u32x4*>(src)[(int)h];
+      const T* e = reinterpret_cast<const T*>(&w);
+      static_for<PER>([&](auto i) { v[h * PER + i] = XType<XT>::up(e[(int)i]); });
+    });
+  } else {
+    static_for<8>([&](auto i) { v[i] = s >= 0 && c + i < p.cols ? XType<XT>::up(src[(int)i]) : 0.f; });
+  }
+}
+
+// |x| as an integer: ordered as the magnitudes are, with infinity and then NaN above all.
+__device__ __forceinline__ u32 mag(float x) { return __builtin_bit_cast(u32, x) & 0x7fffffffu; }
+
+// Maximum over the 16 lanes of a DPP row, in all of them.
+__device__ __forceinline__ u32 row_max(u32 v) {
+  v = max(v, (u32)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, true));  // row_ror:8
+  v = max(v, (u32)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, true));
+  v = max(v, (u32)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, true));
+  return max(v, (u32)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, true));
+}
+
+struct Scale {
+  float scale, inverse;
+  bool bad;
+};
+__device__ __forceinline__ Scale scale_of(u32 top, int pow2) {
+  Scale s;
+  s.bad = top >= 0x7f800000u;
+  if (pow2) {
+    // top = 1.f * 2^e: the least power of two s with top / s <= 448 = 1.75 * 2^8 is 2^(e - 8), one
+    // more when the fraction is above 1.75
+    const int e = (int)(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+    const int c = max(e, -126);
+    s.scale = __builtin_bit_cast(float, (u32)(c + 127) << 23);
+    s.inverse = __builtin_bit_cast(float, (u32)(127 - c) << 23);
+  } else {
+    const float t = fmaxf(__builtin_bit_cast(float, s.bad ? 0u : top), 448.f * 0x1p-126f);
+    s.scale = t / 448.f;
+    s.inverse = 448.f / t;
+  }
+  if (s.bad) s.scale = __builtin_nanf("");
+  return s;
+}
+
+// Four e4m3 codes; the products are rounded to fp32, then to nearest even in the conversion.
+__device__ __forceinline__ u32 codes4(float a, float b, float c, float d, const Scale& s) {
+  if (s.bad) return 0x7f7f7f7fu;
+  auto clip = [&](float v) { return __builtin_amdgcn_fmed3f(v * s.inverse, -448.f, 448.f); };
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(clip(a), clip(b), 0, false);
+  return (u32)__builtin_amdgcn_cvt_pk_fp8_f32(clip(c), clip(d), w, true);
+}
+
+// 8 codes at row r, columns c .. c + 7: those below `cols` data, zeros up to q_cols.
+__device__ __forceinline__ void store8(const QParams& p, int64_t r, int64_t c, u32 lo, u32 hi) {
+  u8* d = p.q + r * p.ldq + c;
+  const uint64_t w = (uint64_t)hi << 32 | lo;
+  if (p.q_vec && c + 8 <= p.q_cols) {
+    *reinterpret_cast<uint64_t*>(d) = w;
+  } else {
+    static_for<8>([&](auto i) { if (c + i < p.q_cols) d[(int)i] = (u8)(w >> (8 * i)); });
+  }
+}
+// Codes past the data are zero even in a block whose scale is NaN.
+__device__ __forceinline__ u32 keep(u32 w, int64_t left) {
+  return left >= 4 ? w : left <= 0 ? 0u : w & (0xffffffffu >> (8 * (4 - (int)left)));
+}
+
+// Scales for each row and 128 columns, row-major: a wave takes 512 columns of a row, a lane 8
+// neighbouring ones, the 16 lanes of a DPP row one block.
+template <int XT>
+__global__ __launch_bounds__(256) void quant_rows(const QParams p, int64_t units, int segs) {
+  const int lane = threadIdx.x & 63;
+  const int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (u >= units) return;
+  const int64_t r = u / segs, c = (u - r * segs) * 512 + lane * 8;
+  float v[8];
+  load8<XT>(p, source_row(p, r), c, v);
+  u32 m = 0;
+  static_for<8>([&](auto i) { m = max(m, mag(v[i])); });
+  const Scale s = scale_of(row_max(m), p.pow2);
+  store8(p, r, c, keep(codes4(v[0], v[1], v[2], v[3], s), p.cols - c),
+         keep(codes4(v[4], v[5], v[6], v[7], s), p.cols - c - 4));
+  if ((lane & 15) == 0 && c < p.cols) p.scale[r * p.scale_r + c / 128 * p.scale_c] = s.scale;
+}
+
+// A 128 x 128 tile: row-major and transposed codes from one read, with scales by row and by
+// column, or one scale for the tile.  Thread (ty, lx) holds rows 8 ty .. + 7 of columns 8 lx .. + 7;
+// the transposed codes go through LDS (chunk ^ column / 8, so that the 16 lanes of a write fall on
+// different banks) and leave as 16-byte chunks.
+template <int XT>
+__global__ __launch_bounds__(256) void quant_tiles(const QParams p, int tiles_c) {
+  __shared__ u32 colmax[128];
+  __shared__ uint64_t turned[128 * 16];
+  const int tid = threadIdx.x, lx = tid & 15, ty = tid >> 4;
+  const int64_t rb = blockIdx.x / tiles_c, cb = blockIdx.x % tiles_c;
+  const int64_t r0 = rb * 128 + ty * 8, c0 = cb * 128 + lx * 8;
+  if (tid < 128) colmax[tid] = 0;
+  float v[8][8];
+  static_for<8>([&](auto i) {
+    const int64_t r = r0 + i;
+    load8<XT>(p, r < p.rows ? source_row(p, r) : -1, c0, v[i]);
+  });
+  __syncthreads();
+  u32 rm[8];
+  static_for<8>([&](auto i) {
+    rm[i] = 0;
+    static_for<8>([&](auto j) { rm[i] = max(rm[i], mag(v[i][j])); });
+  });
+  Scale tile;
+  if (p.block) {
+    u32 m = 0;
+    static_for<8>([&](auto i) { m = max(m, rm[i]); });
+    m = row_max(m);
+    if (lx == 0) atomicMax(&colmax[0], m);  // a maximum: the same whatever the order
+    __syncthreads();
+    tile = scale_of(colmax[0], p.pow2);
+    if (tid == 0) p.scale[rb * p.scale_r + cb * p.scale_c] = tile.scale;
+  } else if (p.qt) {
+    static_for<8>([&](auto j) {
+      u32 m = 0;
+      static_for<8>([&](auto i) { m = max(m, mag(v[i][j])); });
+      m = max(m, (u32)__shfl_xor((int)m, 16, 64));
+      m = max(m, (u32)__shfl_xor((int)m, 32, 64));
+      if ((tid & 48) == 0) atomicMax(&colmax[lx * 8 + j], m);
+    });
+    __syncthreads();
+  }
+  if (p.q) {
+    static_for<8>([&](auto i) {
+      const int64_t r = r0 + i;
+      const Scale s = p.block ? tile : scale_of(row_max(rm[i]), p.pow2);
+      if (r < p.rows) {
+        store8(p, r, c0, keep(codes4(v[i][0], v[i][1], v[i][2], v[i][3], s), p.cols - c0),
+               keep(codes4(v[i][4], v[i][5], v[i][6], v[i][7], s), p.cols - c0 - 4));
+        if (!p.block && lx == 0) p.scale[r * p.scale_r + cb * p.scale_c] = s.scale;
+      }
+    });
+  }
+  if (!p.qt) return;
+  static_for<8>([&](auto j) {
+    const int col = lx * 8 + j;
+    const Scale s = p.block ? tile : scale_of(colmax[col], p.pow2);
+    const u32 lo = keep(codes4(v[0][j], v[1][j], v[2][j], v[3][j], s), p.rows - r0);
+    const u32 hi = keep(codes4(v[4][j], v[5][j], v[6][j], v[7][j], s), p.rows - r0 - 4);
+    turned[col * 16 + (((ty >> 1) ^ (lx & 7)) << 1 | (ty & 1))] = (uint64_t)hi << 32 | lo;
+    if (!p.block && ty == 0 && c0 + j < p.cols)
+      p.scale_t[(c0 + j) * p.scale_t_c + rb * p.scale_t_r] = s.scale;
+  });
+  __syncthreads();
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int q = tid + it * 256, col = q >> 3, ch = q & 7;
+    const int64_t c = cb * 128 + col, r = rb * 128 + ch * 16;
+    if (c >= p.cols || r >= p.qt_cols) continue;
+    const u32x4 w = *reinterpret_cast<const u32x4*>(&turned[col * 16 + ((ch ^ ((col >> 3) & 7)) << 1)]);
+    u8* d = p.qt + c * p.ldqt + r;
+    if (p.qt_vec && r + 16 <= p.qt_cols) {
+      *reinterpret_cast<u32x4*>(d) = w;
+    } else {
+      const u8* e = reinterpret_cast<const u8*>(&w);
+#pragma unroll
+      for (int b = 0; b < 16; ++b)
+        if (r + b < p.qt_cols) d[b] = e[b];
+    }
+  }
+}
+
+template <int XT> hipError_t launch(const QParams& p, hipStream_t s, bool* too_large) {
+  if (!p.block && !p.qt) {
+    const int64_t segs = (p.q_cols + 511) / 512, units = p.rows * segs, blocks = (units + 3) / 4;
+    if (blocks > INT32_MAX) { *too_large = true; return hipSuccess; }
+    hipLaunchKernelGGL(quant_rows<XT>, dim3((unsigned)blocks), dim3(256), 0, s, p, units, (int)segs);
+  } else {
+    const int64_t tc = (p.cols + 127) / 128, blocks = (p.rows + 127) / 128 * tc;
+    if (blocks > INT32_MAX) { *too_large = true; return hipSuccess; }
+    hipLaunchKernelGGL(quant_tiles<XT>, dim3((unsigned)blocks), dim3(256), 0, s, p, (int)tc);
+  }
+  return hipGetLastError();
+}
+
+bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+}  // namespace
+}  // namespace htk
+
+using namespace htk;
+
+extern "C" int quant_blocks(const quant_args* a, void* stream) {
+  if (!a) return GEMM_ERR_INVALID_ARG;
+  constexpr int64_t kMost = INT32_MAX / 2;
+  if (a->rows < 0 || a->cols < 0 || a->rows > kMost || a->cols > kMost) return GEMM_ERR_INVALID_ARG;
+  if (a->block_rows != 1 && a->block_rows != 128) return GEMM_ERR_INVALID_ARG;
+  if ((a->pow2 != 0 && a->pow2 != 1) || (a->pad != 0 && a->pad != 1) || a->index_div < 1) return GEMM_ERR_INVALID_ARG;
+  if (a->row_index && (a->x_rows < 0 || a->x_rows > kMost)) return GEMM_ERR_INVALID_ARG;
+  if (a->x_type != GEMM_F32 && a->x_type != GEMM_F16 && a->x_type != GEMM_BF16) return GEMM_ERR_DTYPE_COMBO;
+  const bool block = a->block_rows == 128;
+  if (a->ldx < a->cols || (a->q && a->ldq < a->cols) || (a->qt && a->ldqt < a->rows)) return GEMM_ERR_LAYOUT;
+  if (a->scale && (a->scale_r < 0 || a->scale_c < 0)) return GEMM_ERR_LAYOUT;
+  if (a->scale_t && (a->scale_t_c < 0 || a->scale_t_r < 0)) return GEMM_ERR_LAYOUT;
+  if (a->rows > 0 && a->cols > 0) {   // buffers of an empty matrix may be NULL
+    if (!a->q && !a->qt) return GEMM_ERR_INVALID_ARG;
+    if (block ? (!a->scale || a->scale_t) : ((a->q != nullptr) != (a->scale != nullptr) ||
+                                             (a->qt != nullptr) != (a->scale_t != nullptr)))
+      return GEMM_ERR_INVALID_ARG;
+    if (!a->x && !(a->row_index && a->x_rows == 0)) return GEMM_ERR_INVALID_ARG;
+  }
+  const int xs = a->x_type == GEMM_F32 ? 4 : 2;
+  if (!on(a->x, xs) || !on(a->scale, 4) || !on(a->scale_t, 4) || !on(a->row_index, 4)) return GEMM_ERR_MISALIGNED;
+  const int rc = arch_status();
+  if (rc) return rc;
+  if (a->rows == 0 || a->cols == 0) return GEMM_OK;
+  QParams p;
+  p.x = a->x;
+  p.index = a->row_index;
+  p.q = static_cast<u8*>(a->q);
+  p.qt = static_cast<u8*>(a->qt);
+  p.scale = a->scale;
+  p.scale_t = a->scale_t;
+  p.rows = a->rows;
+  p.cols = a->cols;
+  p.ldx = a->ldx;
+  p.x_rows = a->x_rows;
+  p.ldq = a->ldq;
+  p.ldqt = a->ldqt;
+  p.q_cols = !a->q ? 0 : a->pad ? std::min(a->ldq, (a->cols + 15) / 16 * 16) : a->cols;
+  p.qt_cols = !a->qt ? 0 : a->pad ? std::min(a->ldqt, (a->rows + 15) / 16 * 16) : a->rows;
+  p.scale_r = a->scale_r;
+  p.scale_c = a->scale_c;
+  p.scale_t_c = a->scale_t_c;
+  p.scale_t_r = a->scale_t_r;
+  p.index_div = a->index_div;
+  p.pow2 = a->pow2;
+  p.block = block;
+  p.x_vec = on(a->x, 16) && a->ldx * xs % 16 == 0;
+  p.q_vec = on(a->q, 8) && a->ldq % 8 == 0;
+  p.qt_vec = on(a->qt, 16) && a->ldqt % 16 == 0;
+  bool too_large = false;
+  hipStream_t s = (hipStream_t)stream;
+  const hipError_t err = a->x_type == GEMM_F32   ? launch<DT_F32>(p, s, &too_large)
+                         : a->x_type == GEMM_F16 ? launch<DT_F16>(p, s, &too_large)
+                                                 : launch<DT_BF16>(p, s, &too_large);
+  if (too_large) return GEMM_ERR_INVALID_ARG;
+  return err == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}

@@ -1,0 +1,666 @@
+// scaled.h -- gfx950 kernels of the block-scaled e4m3 products (htscaled.h).
+//
+//   D(m, n) = act(alpha * rs[m] * sum_b sA(m, b) sB(n, b) * [sum_{k in block b} A(m, k) B(n, k)]
+//                 + beta C(m, n) + bias[n])
+//
+// A block of k is 128 long: exactly one v_mfma_f32_16x16x128_f8f6f4.  Its sum over the block
+// starts from zero and is then added to the fp32 accumulator with one fused multiply-add by
+// sA * sB, so fp32 scales of any value cost 4 VALU operations for each matrix instruction (16 of
+// its 32 issue cycles on a SIMD; they run beside the other wave's, or the next, MFMA).
+//
+// Operands are swapped in the instruction: B's rows (n) are its A operand and A's rows (m) its B
+// operand.  A lane's four accumulators are then four neighbouring n of one m: one A scale
+// serves them all, a 128-wide B scale is the same for the whole wave, and the outputs of a lane
+// are contiguous in D.
+#pragma once
+
+#include "kernels.h"
+
+namespace htk {
+
+constexpr int kSB = 128;  // values of k per scale
+
+struct SParams {
+  const u8* A;
+  const u8* B;
+  const float* a_scale;
+  const float* b_scale;
+  const void* C;             // nullptr: not read
+  void* D;
+  const void* bias;          // nullptr: none
+  const float* row_scale;    // nullptr: none
+  const int32_t* offsets;    // groups
+  float* workspace;          // fp32 planes, split_k > 1
+  int64_t M, N, K;
+  int64_t lda, ldb, ldc, ldd;
+  int64_t a_sm, a_sk, b_sn, b_sk;
+  int64_t a_l, b_l, c_l, d_l, as_l, bs_l;  // elements from one product to the next
+  float alpha, beta;
+  int act, form, groups;
+  int tiles_m, tiles_n;
+  int split_k, blocks_per_split;           // slices of k, in blocks of 128
+};
+
+enum : int { FORM_SINGLE = 0, FORM_BATCH = 1, FORM_ROWS = 2, FORM_K = 3 };
+
+// One workgroup's share: its product's operands, its tile and its blocks of k.
+struct STile {
+  const u8* A;               // row 0 of the product (group), k = 0
+  const u8* B;
+  const float* a_scale;
+  const float* b_scale;
+  const void* C;
+  void* D;
+  const float* row_scale;
+  int64_t M;                 // rows of this product or group
+  int64_t m0, n0;
+  int64_t k0, k1;            // k0 a multiple of 128
+};
+
+__device__ __forceinline__ int wave_max_scan(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d, 64);
+    if (lane >= d) v = max(v, o);
+  }
+  return v;
+}
+__device__ __forceinline__ int wave_sum_scan(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d, 64);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// Workgroup id -> place in the tile order: ids are dealt to the 8 XCDs in turn, and each XCD gets
+// a contiguous range, so that neighbours in the order share an L2.
+__device__ __forceinline__ int xcd_order(int pid, int n) {
+  const int per = n >> 3, extra = n & 7, x = pid & 7;
+  return x * per + min(x, extra) + (pid >> 3);
+}
+// Tile t of a product with tm x tn tiles: 4 tile rows at a time, column by column.
+__device__ __forceinline__ void walk_tiles(int t, int tm, int tn, int& m, int& n) {
+  const int width = 4 * tn, group = t / width, first = group * 4;
+  const int rows = min(tm - first, 4), within = t - group * width;
+  m = first + within % rows;
+  n = within / rows;
+}
+
+// The tile of this workgroup; false for one that has none (it exits before its first barrier).
+// Groups of rows: every wave scans the offsets, 64 groups at a time, for the number of tiles and
+// then for the group that holds its own; no launch before the product is needed for it.
+template <int BM, int BN, class OT>
+__device__ __forceinline__ bool tile_share(const SParams& p, STile& s) {
+  s.A = p.A;
+  s.B = p.B;
+  s.a_scale = p.a_scale;
+  s.b_scale = p.b_scale;
+  s.C = p.C;
+  s.D = p.D;
+  s.row_scale = p.row_scale;
+  s.M = p.M;
+  s.k0 = 0;
+  s.k1 = p.K;
+  int tm = p.tiles_m, t;
+  const int lane = threadIdx.x & 63;
+  if (p.form == FORM_ROWS) {
+    const int G = p.groups, M = (int)p.M;
+    const int first = min(max(p.offsets[0], 0), M);
+    int total = 0, top = first;
+    for (int c = 0; c < G; c += 64) {
+      const int v = c + lane < G ? min(max(p.offsets[c + lane + 1], 0), M) : 0;
+      const int hi = max(wave_max_scan(v, lane), top);
+      int lo = __shfl_up(hi, 1, 64);
+      if (lane == 0) lo = top;
+      const int n = c + lane < G ? (hi - lo + BM - 1) / BM * p.tiles_n : 0;
+      total += __shfl(wave_sum_scan(n, lane), 63, 64);
+      top = __shfl(hi, 63, 64);
+    }
+    if ((int)blockIdx.x >= total) return false;
+    t = xcd_order(blockIdx.x, total);
+    int before = 0, e = 0, lo_e = 0, hi_e = 0;
+    top = first;
+    for (int c = 0; c < G; c += 64) {
+      const int v = c + lane < G ? min(max(p.offsets[c + lane + 1], 0), M) : 0;
+      const int hi = max(wave_max_scan(v, lane), top);
+      int lo = __shfl_up(hi, 1, 64);
+      if (lane == 0) lo = top;
+      const int n = c + lane < G ? (hi - lo + BM - 1) / BM * p.tiles_n : 0;
+      const int sum = wave_sum_scan(n, lane);
+      const unsigned long long past = __ballot(before + sum > t);
+      if (past != 0) {
+        const int l = __ffsll(past) - 1;
+        e = c + l;
+        lo_e = __shfl(lo, l, 64);
+        hi_e = __shfl(hi, l, 64);
+        t -= before + __shfl(sum - n, l, 64);
+        break;
+      }
+      before += __shfl(sum, 63, 64);
+      top = __shfl(hi, 63, 64);
+    }
+    e = __builtin_amdgcn_readfirstlane(e);
+    lo_e = __builtin_amdgcn_readfirstlane(lo_e);
+    hi_e = __builtin_amdgcn_readfirstlane(hi_e);
+    t = __builtin_amdgcn_readfirstlane(t);
+    s.A += (int64_t)lo_e * p.lda;
+    s.a_scale += (int64_t)lo_e * p.a_sm;
+    s.B += e * p.b_l;
+    s.b_scale += e * p.bs_l;
+    if (s.C) s.C = (const OT*)s.C + (int64_t)lo_e * p.ldc;
+    s.D = (OT*)s.D + (int64_t)lo_e * p.ldd;
+    if (s.row_scale) s.row_scale += lo_e;
+    s.M = hi_e - lo_e;
+    tm = (int)((s.M + BM - 1) / BM);
+  } else {
+    const int64_t z = blockIdx.z;
+    if (p.form == FORM_BATCH) {
+      s.A += z * p.a_l;
+      s.B += z * p.b_l;
+      s.a_scale += z * p.as_l;
+      s.b_scale += z * p.bs_l;
+    }
+    if (p.form != FORM_SINGLE) {
+      if (s.C) s.C = (const OT*)s.C + z * p.c_l;
+      s.D = (OT*)s.D + z * p.d_l;
+    }
+    if (p.form == FORM_K) {
+      int lo = 0, hi = 0;
+      const int K = (int)p.K;
+      for (int i = lane; i <= (int)z + 1; i += 64) {
+        const int v = min(max(p.offsets[i], 0), K);
+        hi = max(hi, v);
+        if (i <= (int)z) lo = max(lo, v);
+      }
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) {
+        lo = max(lo, __shfl_xor(lo, d, 64));
+        hi = max(hi, __shfl_xor(hi, d, 64));
+      }
+      lo = __builtin_amdgcn_readfirstlane(lo);
+      hi = __builtin_amdgcn_readfirstlane(hi);
+      // an end at K itself may lie inside a block; a group that starts there is empty
+      s.k0 = lo == K ? (K + kSB - 1) / kSB * (int64_t)kSB : lo / kSB * kSB;
+      s.k1 = hi == K ? K : hi / kSB * kSB;
+      if (s.k1 < s.k0) s.k1 = s.k0;
+    }
+    if (p.split_k > 1) {
+      s.k0 = min((int64_t)blockIdx.y * p.blocks_per_split * kSB, p.K);
+      s.k1 = min(s.k0 + (int64_t)p.blocks_per_split * kSB, p.K);
+    }
+    t = xcd_order(blockIdx.x, gridDim.x);
+  }
+  int m, n;
+  walk_tiles(t, tm, p.tiles_n, m, n);
+  s.m0 = (int64_t)m * BM;
+  s.n0 = (int64_t)n * BN;
+  return true;
+}
+
+// C, bias and D of either output type.
+template <class OT> struct SOut;
+template <> struct SOut<u16> {
+  __device__ static float load(const void* p, int64_t i) { return bf16_to_f32(((const u16*)p)[i]); }
+  __device__ static u16 bits(float v) { return f32_to_bf16(v); }
+};
+template <> struct SOut<float> {
+  __device__ static float load(const void* p, int64_t i) { return ((const float*)p)[i]; }
+  __device__ static float bits(float v) { return v; }
+};
+
+// One output from its fp32 sum; rounded once, to D's type.
+template <class OT>
+__device__ __forceinline__ void finish_one(const SParams& p, const STile& s, int64_t row, int64_t col, float sum) {
+  float v = p.alpha * sum;
+  if (s.row_scale) v *= s.row_scale[row];
+  if (s.C) v += p.beta * SOut<OT>::load(s.C, row * p.ldc + col);
+  if (p.bias) v += SOut<OT>::load(p.bias, col);
+  ((OT*)s.D)[row * p.ldd + col] = SOut<OT>::bits(activate(p.act, v));
+}
+
+// One block of k of a 16 x 16 piece: the fragments of a lane (32 codes of one row) and their
+// product.  The 8-bit matrix instructions align the products of a group before they add them and
+// keep about 14 bits of the largest (measured on random codes: 1.3e-5 to 5.6e-5 of the sum's size
+// for every fp8 form, 16x16x128, 32x32x64, 16x16x32 and 32x32x16 alike).  That is 40 times below
+// half a step of a bf16 D, so bf16 outputs take the 8-bit instruction; fp32 outputs take the
+// codes as bf16, which holds them exactly, through the bf16 instruction at half the rate, whose
+// sums keep fp32 (1e-8 to 8e-8 in the same measurement).
+template <class OT> struct Frag;
+template <> struct Frag<u16> {
+  u32x4 w[2];
+  __device__ __forceinline__ void set(int u, const u32x4& v) { w[u] = v; }
+};
+__device__ __forceinline__ f32x4 mfma_block(const Frag<u16>& n, const Frag<u16>& m) {
+  f32x4 c = {0.f, 0.f, 0.f, 0.f};
+  Atom<DT_F8, 16>::mma(c, n.w, m.w, 0);
+  return c;
+}
+template <> struct Frag<float> {
+  bf16x8 w[4];
+  __device__ __forceinline__ void set(int u, const u32x4& v) {
+    static_for<2>([&](auto h) {
+      static_for<2>([&](auto d) {
+        static_for<2>([&](auto s) {
+          const auto two = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * h + d], 1.0f, s != 0);
+          w[2 * u + h][4 * d + 2 * s] = two[0];
+          w[2 * u + h][4 * d + 2 * s + 1] = two[1];
+        });
+      });
+    });
+  }
+};
+__device__ __forceinline__ f32x4 mfma_block(const Frag<float>& n, const Frag<float>& m) {
+  f32x4 c = {0.f, 0.f, 0.f, 0.f};
+  static_for<4>([&](auto q) { c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(n.w[q], m.w[q], c, 0, 0, 0); });
+  return c;
+}
+
+// ------------------------------------------------------------------------------------------
+// Any alignment: 64 x 64 tiles, single-byte predicated loads through registers into LDS.  The
+// kernel for operands that the 16-byte loads cannot read, and the plainest form of the
+// operation: one block of k at a time, two barriers each.
+// ------------------------------------------------------------------------------------------
+template <class OT>
+__global__ __launch_bounds__(256) void scaled_narrow(const SParams p, int b_block) {
+  __shared__ u32x4 lds[128 * 8];              // 64 rows of A, then 64 rows of B
+  STile s;
+  if (!tile_share<64, 64, OT>(p, s)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
+  const int x = lane & 15, g = lane >> 4;
+  f32x4 acc[2][2];
+  static_for<2>([&](auto i) { static_for<2>([&](auto j) { acc[i][j] = f32x4{}; }); });
+  for (int64_t k = s.k0; k < s.k1; k += kSB) {
+#pragma unroll 1
+    for (int q = tid; q < 128 * 8; q += 256) {
+      const int row = q >> 3, c = q & 7;
+      const int64_t r = row < 64 ? s.m0 + row : s.n0 + row - 64;
+      const bool live = r < (row < 64 ? s.M : p.N);
+      const u8* src = (row < 64 ? s.A + r * p.lda : s.B + r * p.ldb) + k + c * 16;
+      u32x4 v;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        u32 w = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (live && k + c * 16 + d * 4 + b < s.k1) w |= (u32)src[d * 4 + b] << (8 * b);
+        v[d] = w;
+      }
+      lds[swizzled_slot<8>(row, c)] = v;
+    }
+    __syncthreads();
+    const int64_t kb = k / kSB;
+    float sa[2];
+    f32x4 sb[2];
+    static_for<2>([&](auto i) {
+      const int64_t m = s.m0 + wm + i * 16 + x;
+      sa[i] = m < s.M ? s.a_scale[m * p.a_sm + kb * p.a_sk] : 0.f;
+      static_for<4>([&](auto r) {
+        const int64_t n = s.n0 + wn + i * 16 + g * 4 + r;
+        sb[i][(int)r] = n < p.N ? s.b_scale[(b_block == 1 ? n : n / kSB) * p.b_sn + kb * p.b_sk] : 0.f;
+      });
+    });
+    Frag<OT> fa[2], fb[2];
+    static_for<2>([&](auto i) {
+      static_for<2>([&](auto u) {
+        fa[i].set(u, lds[swizzled_slot<8>(wm + i * 16 + x, g + 4 * u)]);
+        fb[i].set(u, lds[swizzled_slot<8>(64 + wn + i * 16 + x, g + 4 * u)]);
+      });
+    });
+    static_for<2>([&](auto i) {
+      static_for<2>([&](auto j) {
+        const f32x4 t = mfma_block(fb[j], fa[i]);
+        static_for<4>([&](auto r) {
+          acc[i][j][(int)r] = __builtin_fmaf(t[(int)r], sa[i] * sb[j][(int)r], acc[i][j][(int)r]);
+        });
+      });
+    });
+    __syncthreads();
+  }
+  static_for<2>([&](auto i) {
+    static_for<2>([&](auto j) {
+      static_for<4>([&](auto r) {
+        const int64_t m = s.m0 + wm + i * 16 + x, n = s.n0 + wn + j * 16 + g * 4 + r;
+        if (m < s.M && n < p.N) finish_one<OT>(p, s, m, n, acc[i][j][(int)r]);
+      });
+    });
+  });
+}
+
+// ------------------------------------------------------------------------------------------
+// The outputs of a lane: RM rows m, and for each of them 4 RN neighbouring columns.  Whole
+// 16-byte stores where D allows them; four lane groups cover 16 RN neighbouring columns of a row.
+// ------------------------------------------------------------------------------------------
+template <class OT, int RM, int RN, class RowOf>
+__device__ __forceinline__ void store_outputs(const SParams& p, const STile& s, f32x4 (&acc)[RM][RN],
+                                              RowOf row_of, int64_t col0) {
+  constexpr int NV = 4 * RN;                 // outputs of a lane in one row
+  constexpr int VO = 16 / (int)sizeof(OT);   // outputs in 16 bytes
+  const bool whole = col0 + NV <= p.N;
+  const bool d_vec = whole && NV % VO == 0 && p.ldd % VO == 0 && (reinterpret_cast<uintptr_t>(s.D) & 15) == 0;
+  if (p.split_k > 1) {
+    float* w = p.workspace + (int64_t)blockIdx.y * p.M * p.N;
+    static_for<RM>([&](auto i) {
+      const int64_t row = row_of(i);
+      if (row < s.M)
+        static_for<RN>([&](auto j) {
+          if (whole && p.N % 4 == 0) {
+            *reinterpret_cast<f32x4*>(w + row * p.N + col0 + 4 * j) = acc[i][j];
+          } else {
+            static_for<4>([&](auto r) {
+              if (col0 + 4 * j + r < p.N) w[row * p.N + col0 + 4 * j + r] = acc[i][j][(int)r];
+            });
+          }
+        });
+    });
+    return;
+  }
+  float bias[NV];
+  static_for<NV>([&](auto c) { bias[c] = p.bias && col0 + c < p.N ? SOut<OT>::load(p.bias, col0 + c) : 0.f; });
+  static_for<RM>([&](auto i) {
+    const int64_t row = row_of(i);
+    if (row < s.M) {
+      const float a = p.alpha, rs = s.row_scale ? s.row_scale[row] : 1.f;
+      float v[NV];
+      static_for<NV>([&](auto c) { v[c] = acc[i][c / 4][c % 4] * a * rs; });
+      if (s.C) static_for<NV>([&](auto c) {
+        if (col0 + c < p.N) v[c] += p.beta * SOut<OT>::load(s.C, row * p.ldc + col0 + c);
+      });
+      static_for<NV>([&](auto c) { v[c] += bias[c]; });
+      if (p.act == 2) static_for<NV>([&](auto c) { v[c] = gelu(v[c]); });
+      else if (p.act == 1) static_for<NV>([&](auto c) { v[c] = relu(v[c]); });
+      else if (p.act == 3) static_for<NV>([&](auto c) { v[c] = silu(v[c]); });
+      OT* d = (OT*)s.D + row * p.ldd + col0;
+      if (d_vec) {
+        static_for<(NV + VO - 1) / VO>([&](auto q) {
+          OT o[VO];
+          static_for<VO>([&](auto c) { o[c] = SOut<OT>::bits(v[(q * VO + c) % NV]); });
+          *reinterpret_cast<u32x4*>(d + q * VO) = *reinterpret_cast<const u32x4*>(o);
+        });
+      } else {
+        static_for<NV>([&](auto c) { if (col0 + c < p.N) d[(int)c] = SOut<OT>::bits(v[c]); });
+      }
+    }
+  });
+}
+
+typedef __attribute__((address_space(1))) const void gbl_void_t;
+
+// ------------------------------------------------------------------------------------------
+// Tiled kernel: BM x BN outputs by WM x WN waves, blocks of k in a ring of ST LDS stages filled
+// by DMA, one barrier per block.  A stage holds the BM + BN rows of 128 bytes (XOR-swizzled
+// chunks) and their BM + BN scales, fetched by 4-byte DMA so that scales may have any strides.
+//
+// Rows are placed in LDS so that a lane's rows are neighbours: LDS row i * 16 + x of a wave's A
+// tile is its row x * RM + i, and LDS row j * 16 + y of its B tile is its row
+// (y / 4) * 4 RN + 4 j + y % 4.  The lane's A scales (and per-column B scales) are then
+// contiguous in LDS, and its outputs in D.  The placement costs nothing: every DMA lane has its
+// own source address.
+// ------------------------------------------------------------------------------------------
+template <int BM, int BN, int WM, int WN, int ST, int BB, class OT, int OCC>
+__global__ __launch_bounds__(WM * WN * 64, OCC) void scaled_tile(const SParams p) {
+  constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, RM = TM / 16, RN = TN / 16;
+  constexpr int OPS_T = (BM + BN) / 8 / NW;          // tile DMA instructions per wave and block
+  constexpr int SCI = (BM + BN) / 64;                // scale DMA instructions per block
+  constexpr int OPS_S = (SCI + NW - 1) / NW;
+  constexpr int OPS = OPS_T + OPS_S;
+  constexpr int STAGE = (BM + BN) * 8 + (BM + BN) / 4;  // 16-byte chunks
+  static_assert((BM + BN) % (8 * NW) == 0 && BM % 64 == 0 && BN % 64 == 0, "DMA blocks over the waves");
+  static_assert(TN <= kSB && kSB % TN == 0, "one 128-wide B scale per wave");
+  __shared__ u32x4 lds[ST * STAGE];
+  STile s;
+  if (!tile_share<BM, BN, OT>(p, s)) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int x = lane & 15, g = lane >> 4;
+
+  const char* a_tile = uniform_ptr((const char*)s.A + s.m0 * p.lda + s.k0);
+  const char* b_tile = uniform_ptr((const char*)s.B + s.n0 * p.ldb + s.k0);
+  const int64_t K = uniform_i64(s.k1 - s.k0);
+  const int64_t a_span = uniform_i64((s.M - s.m0 - 1) * p.lda + K);
+  const int64_t b_span = uniform_i64((p.N - s.n0 - 1) * p.ldb + K);
+  const int nk = (int)((K + kSB - 1) / kSB);
+
+  // DMA instruction i of this wave fills LDS rows 8 blk .. 8 blk + 7 (A's, then B's), blk =
+  // wave + NW i: lane l row 8 blk + l / 8, slot l % 8, which holds chunk (l % 8) ^ key(row).
+  uint32_t off[OPS_T];
+  const int chunk = (lane & 7) ^ row_key<8>((wave & 1) * 8 + (lane >> 3));
+  static_for<OPS_T>([&](auto i) {
+    const int R = (wave + NW * i) * 8 + (lane >> 3);
+    if (R < BM) {
+      const int w = R / TM, q = R % TM;
+      off[i] = (uint32_t)((w * TM + (q & 15) * RM + (q >> 4)) * p.lda) + chunk * 16;
+    } else {
+      const int w = (R - BM) / TN, q = (R - BM) % TN, y = q & 15;
+      off[i] = (uint32_t)((w * TN + (y >> 2) * (4 * RN) + (q >> 4) * 4 + (y & 3)) * p.ldb) + chunk * 16;
+    }
+  });
+  static_assert(NW % 2 == 0, "the row key of a wave's DMA blocks is the same in all of them");
+  // scale addresses: lane l of instruction i fetches scale 64 i + l (A's rows, then B's)
+  const float* sc_ptr[OPS_S];
+  int64_t sc_step[OPS_S];
+  const int64_t kb0 = s.k0 / kSB;
+  static_for<OPS_S>([&](auto i) {
+    const int q = ((wave + NW * i) % SCI) * 64 + lane;
+    if (q < BM) {
+      const int64_t m = min(s.m0 + q, s.M - 1);
+      sc_ptr[i] = s.a_scale + m * p.a_sm + kb0 * p.a_sk;
+      sc_step[i] = p.a_sk;
+    } else {
+      const int64_t n = min(s.n0 + q - BM, p.N - 1);
+      sc_ptr[i] = s.b_scale + (BB == 1 ? n : n / kSB) * p.b_sn + kb0 * p.b_sk;
+      sc_step[i] = p.b_sk;
+    }
+  });
+  // Blocks past the last are issued as zeros, so that the wait counts are the same throughout.
+  auto dma = [&](int t, int stage) {
+    u32x4* st = lds + stage * STAGE;
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(a_tile, a_span), rb = make_rsrc(b_tile, b_span);
+    const int64_t k = (int64_t)t * kSB;
+    const bool in_k = k + chunk * 16 < K;
+    static_for<OPS_T>([&](auto i) {
+      const int blk = wave + NW * i;
+      const uint32_t o = in_k ? off[i] : kOobOffset;
+      if ((NW * i + NW) * 8 <= BM || blk * 8 < BM)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(st + blk * 64), 16, o, (int)k, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void_t*)(st + blk * 64), 16, o, (int)k, 0, 0);
+    });
+    static_for<OPS_S>([&](auto i) {
+      const int ins = (wave + NW * i) % SCI;
+      const float* src = sc_ptr[i] + (int64_t)min(t, nk - 1) * sc_step[i];
+      __builtin_amdgcn_global_load_lds((gbl_void_t*)src, (lds_void_t*)(st + (BM + BN) * 8 + ins * 16), 4, 0, 0);
+    });
+  };
+
+  f32x4 acc[RM][RN];
+  static_for<RM>([&](auto i) { static_for<RN>([&](auto j) { acc[i][j] = f32x4{}; }); });
+  int slot[2];
+  static_for<2>([&](auto u) { slot[u] = swizzled_slot<8>(x, g + 4 * u); });
+
+  auto compute = [&](int stage) {
+    const u32x4* st = lds + stage * STAGE;
+    const u32x4* la = st + wm * TM * 8;
+    const u32x4* lb = st + (BM + wn * TN) * 8;
+    const float* ls = reinterpret_cast<const float*>(st + (BM + BN) * 8);
+    Frag<OT> fb[RN];
+    static_for<RN>([&](auto j) { static_for<2>([&](auto u) { fb[j].set(u, lb[j * 128 + slot[u]]); }); });
+    float sa[RM];
+    static_for<RM>([&](auto i) { sa[i] = ls[wm * TM + x * RM + i]; });
+    f32x4 sb[BB == 1 ? RN : 1];
+    if constexpr (BB == 1) {
+      static_for<RN>([&](auto j) { sb[j] = *reinterpret_cast<const f32x4*>(&ls[BM + wn * TN + g * 4 * RN + 4 * j]); });
+    } else {
+      const float one = ls[BM + wn * TN];
+      static_for<RM>([&](auto i) { sa[i] *= one; });
+    }
+    static_for<RM>([&](auto i) {
+      Frag<OT> fa;
+      static_for<2>([&](auto u) { fa.set(u, la[i * 128 + slot[u]]); });
+      f32x4 t[RN];
+      static_for<RN>([&](auto j) { t[j] = mfma_block(fb[j], fa); });
+      static_for<RN>([&](auto j) {
+        static_for<4>([&](auto r) {
+          const float w = BB == 1 ? sa[i] * sb[BB == 1 ? (int)j : 0][(int)r] : sa[i];
+          acc[i][j][(int)r] = __builtin_fmaf(t[j][(int)r], w, acc[i][j][(int)r]);
+        });
+      });
+    });
+  };
+
+  if (nk > 0) {
+    static_for<ST - 1>([&](auto q) { dma(q, q); });
+    int stage = 0;
+    for (int t = 0; t < nk; ++t) {
+      // block t has landed for this wave and, behind the barrier, for all; the stage refilled
+      // next was last read before it
+      wait_counts<(ST - 2) * OPS, true>();
+      barrier_nofence();
+      int next = stage + ST - 1;
+      if (next >= ST) next -= ST;
+      dma(t + ST - 1, next);
+      compute(stage);
+      if (++stage == ST) stage = 0;
+    }
+    wait_counts<0, true>();  // zero blocks issued past the end
+  }
+  store_outputs<OT, RM, RN>(p, s, acc, [&](auto i) { return s.m0 + wm * TM + x * RM + i; },
+                            s.n0 + wn * TN + g * 4 * RN);
+}
+
+// ------------------------------------------------------------------------------------------
+// Streaming kernel for few rows (decode): the cost is reading B once.  A workgroup owns 16 NBW
+// columns and 16 RM rows; its WK waves take slices of k, each streaming its blocks of B (and the
+// L2-resident rows of A) through a private LDS ring of R blocks by DMA, with no barrier in the
+// loop.  The partial sums meet in LDS.
+// ------------------------------------------------------------------------------------------
+template <int RM, int NBW, int WK, int R, int BB, class OT, int OCC>
+__global__ __launch_bounds__(WK * 64, OCC) void scaled_stream(const SParams p) {
+  constexpr int BM = 16 * RM, BN = 16 * NBW, ROWS = BM + BN;
+  constexpr int OPS_S = (ROWS + 63) / 64, OPS = ROWS / 8 + OPS_S;
+  constexpr int BLK = ROWS * 8 + OPS_S * 16;         // 16-byte chunks of a ring block
+  constexpr int NT = WK * 64;
+  static_assert(R >= 2 && (R - 2) * OPS < 64, "vmcnt range");
+  static_assert(BN <= kSB && kSB % BN == 0, "one 128-wide B scale per workgroup");
+  __shared__ u32x4 ring[WK][R][BLK];
+  STile s;
+  if (!tile_share<BM, BN, OT>(p, s)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int x = lane & 15, g = lane >> 4;
+  const int64_t K = uniform_i64(s.k1 - s.k0);
+  const int nb = (int)((K + kSB - 1) / kSB), per = (nb + WK - 1) / WK;
+  const int b0 = wave * per, nloc = max(0, min(b0 + per, nb) - b0);
+
+  const char* a_tile = uniform_ptr((const char*)s.A + s.m0 * p.lda + s.k0);
+  const char* b_tile = uniform_ptr((const char*)s.B + s.n0 * p.ldb + s.k0);
+  const int64_t a_span = uniform_i64((s.M - s.m0 - 1) * p.lda + K);
+  const int64_t b_span = uniform_i64((p.N - s.n0 - 1) * p.ldb + K);
+  const float* sc_ptr[OPS_S];
+  int64_t sc_step[OPS_S];
+  const int64_t kb0 = s.k0 / kSB + b0;
+  static_for<OPS_S>([&](auto i) {
+    const int q = i * 64 + lane;
+    if (q < BN) {                                     // B's rows first, as in the ring block
+      const int64_t n = min(s.n0 + q, p.N - 1);
+      sc_ptr[i] = s.b_scale + (BB == 1 ? n : n / kSB) * p.b_sn + kb0 * p.b_sk;
+      sc_step[i] = p.b_sk;
+    } else {
+      const int64_t m = min(s.m0 + q - BN, s.M - 1);
+      sc_ptr[i] = s.a_scale + m * p.a_sm + kb0 * p.a_sk;
+      sc_step[i] = p.a_sk;
+    }
+  });
+  auto issue = [&](int j, auto slot) {
+    const bool live = j < nloc;
+    const int64_t kb = (int64_t)(b0 + j) * kSB;
+    const int sk = live ? (int)kb : 0;
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(a_tile, a_span), rb = make_rsrc(b_tile, b_span);
+    static_for<ROWS / 8>([&](auto c) {
+      constexpr bool IS_A = c * 8 >= BN;
+      const int row = 8 * c + (lane >> 3), src = IS_A ? row - BN : row;
+      const int ch = (lane & 7) ^ row_key<8>(row);
+      const uint32_t o = live && kb + ch * 16 < K ? (uint32_t)(src * (IS_A ? p.lda : p.ldb)) + ch * 16 : kOobOffset;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(IS_A ? ra : rb, (lds_void_t*)(&ring[wave][slot][c * 64]), 16, o, sk, 0, 0);
+    });
+    const int js = max(0, min(j, nloc - 1));
+    if (nloc > 0)
+      static_for<OPS_S>([&](auto i) {
+        __builtin_amdgcn_global_load_lds((gbl_void_t*)(sc_ptr[i] + js * sc_step[i]),
+                                         (lds_void_t*)(&ring[wave][slot][ROWS * 8 + i * 16]), 4, 0, 0);
+      });
+  };
+  f32x4 acc[RM][NBW];
+  static_for<RM>([&](auto i) { static_for<NBW>([&](auto j) { acc[i][j] = f32x4{}; }); });
+  auto compute = [&](auto slot) {
+    const u32x4* blk = &ring[wave][slot][0];
+    const float* ls = reinterpret_cast<const float*>(blk + ROWS * 8);
+    Frag<OT> fb[NBW];
+    static_for<NBW>([&](auto j) {
+      static_for<2>([&](auto u) { fb[j].set(u, blk[swizzled_slot<8>(j * 16 + x, g + 4 * u)]); });
+    });
+    static_for<RM>([&](auto i) {
+      Frag<OT> fa;
+      static_for<2>([&](auto u) { fa.set(u, blk[swizzled_slot<8>(BN + i * 16 + x, g + 4 * u)]); });
+      const float sa = ls[BN + i * 16 + x];
+      static_for<NBW>([&](auto j) {
+        const f32x4 t = mfma_block(fb[j], fa);
+        static_for<4>([&](auto r) {
+          const float w = sa * ls[BB == 1 ? j * 16 + g * 4 + (int)r : 0];
+          acc[i][j][(int)r] = __builtin_fmaf(t[(int)r], w, acc[i][j][(int)r]);
+        });
+      });
+    });
+  };
+  static_for<R - 1>([&](auto q) { issue(q, q); });
+  for (int j = 0; j < nloc; j += R) {
+    static_for<R>([&](auto q) {
+      wait_counts<(R - 2) * OPS, true>();
+      issue(j + q + R - 1, std::integral_constant<int, (q + R - 1) % R>{});
+      if (j + q < nloc) compute(q);
+    });
+  }
+  wait_counts<0, true>();
+  __syncthreads();
+  // [WK][BM][BN + 4]: rows padded by 16 bytes, so that the 16 rows a store instruction writes
+  // spread over the banks
+  constexpr int PITCH = BN + 4;
+  static_assert(sizeof(ring) >= sizeof(float) * WK * BM * PITCH, "partial sums fit the ring");
+  float* part = reinterpret_cast<float*>(&ring[0][0][0]);
+  static_for<RM>([&](auto i) {
+    static_for<NBW>([&](auto j) {
+      *reinterpret_cast<f32x4*>(&part[(wave * BM + i * 16 + x) * PITCH + j * 16 + g * 4]) = acc[i][j];
+    });
+  });
+  __syncthreads();
+  for (int q = tid; q < BM * BN; q += NT) {
+    const int row = q / BN, c = q % BN;
+    const int64_t m = s.m0 + row, n = s.n0 + c;
+    if (m >= s.M || n >= p.N) continue;
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < WK; ++w) sum += part[(w * BM + row) * PITCH + c];
+    if (p.split_k > 1) p.workspace[((int64_t)blockIdx.y * p.M + m) * p.N + n] = sum;
+    else finish_one<OT>(p, s, m, n, sum);
+  }
+}
+
+// The planes of a split k, added in order, and the epilogue.
+template <class OT>
+__global__ __launch_bounds__(256) void scaled_join(const SParams p) {
+  STile s;
+  s.C = p.C;
+  s.D = p.D;
+  s.row_scale = p.row_scale;
+  const int64_t MN = p.M * p.N;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < MN; e += (int64_t)gridDim.x * 256) {
+    const int64_t row = e / p.N, col = e - row * p.N;
+    float sum = 0.f;
+    for (int q = 0; q < p.split_k; ++q) sum += p.workspace[q * MN + e];
+    finish_one<OT>(p, s, row, col, sum);
+  }
+}
+
+}  // namespace htk
