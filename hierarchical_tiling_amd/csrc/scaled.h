@@ -647,6 +647,156 @@ __global__ __launch_bounds__(WK * 64, OCC) void scaled_stream(const SParams p) {
   }
 }
 
+// ------------------------------------------------------------------------------------------
+// Ping-pong kernel, 256 x 256 outputs, 128-wide B scales, bf16 out: two groups of four waves, one
+// wave of each on every SIMD, take turns between a read phase (fragments from LDS, DMA, scales)
+// and a compute phase (matrix instructions and the multiply-adds of their sums), a barrier
+// between phases; group 1 runs one phase behind group 0.  Group g computes rows [128 g, 128 g +
+// 128), wave q of it columns [64 q, 64 q + 64).
+//
+// The accumulators (128 registers), the scales and the instruction's own sums leave no room for
+// all fragments of a block, so a wave holds its B fragments and the first A fragments from the
+// read phase and reads the other A fragments while it computes.  LDS (160 KiB): each A half in
+// two slots, B in three.
+//   * Half g of A(v) is read by group g in its read and compute phases of v (2v + g, 2v + g + 1).
+//     Group g issues half g of A(v + 1) in its read phase of v -- the slot's last reader was its
+//     compute phase of v - 1 -- and waits for it at the end of its compute phase of v.
+//   * B(v) is read in phases 2v and 2v + 1.  Each group issues its half of B(v + 2) in its read
+//     phase of v (the slot held B(v - 1)) and waits for it at the end of its read phase of v + 1.
+// A read phase issues 3 scale loads, 4 DMAs of A and 4 of B, in that order, so "A(v + 1) is
+// there" is at most 4 in flight at the end of the compute phase, and "B(v + 1) is there" at most
+// 11 at the end of the read phase.  Blocks past the end are issued as zeros to keep the counts.
+// ------------------------------------------------------------------------------------------
+template <class OT>
+__global__ __launch_bounds__(512, 1) void scaled_pp(const SParams p) {
+  constexpr int BM = 256, BN = 256, RM = 8, RN = 4, HALF = 128 * 8, B0 = 4 * HALF;
+  __shared__ u32x4 lds[10 * HALF];
+  STile s;
+  if (!tile_share<BM, BN, OT>(p, s)) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = wave >> 2, wq = wave & 3;
+  const int x = lane & 15, c4 = lane >> 4;
+  const char* a_tile = uniform_ptr((const char*)s.A + s.m0 * p.lda + s.k0);
+  const char* b_tile = uniform_ptr((const char*)s.B + s.n0 * p.ldb + s.k0);
+  const int64_t K = uniform_i64(s.k1 - s.k0);
+  const int64_t a_span = uniform_i64((s.M - s.m0 - 1) * p.lda + K);
+  const int64_t b_span = uniform_i64((p.N - s.n0 - 1) * p.ldb + K);
+  const int nk = (int)((K + kSB - 1) / kSB);
+  const int64_t kb0 = s.k0 / kSB;
+  // scales of this lane's rows m0 + 128 g + 8 x .. + 7, and of this wave's columns
+  const char* sa_base = uniform_ptr((const char*)(s.a_scale + s.m0 + kb0 * p.a_sk));
+  const char* sb_base = uniform_ptr((const char*)(s.b_scale + min(s.n0 + wq * 64, p.N - 1) / kSB * p.b_sn + kb0 * p.b_sk));
+  const int64_t sa_span = uniform_i64((s.M - s.m0) * 4);
+  const uint32_t sa_off = (uint32_t)(g * 128 + x * 8) * 4;
+
+  // LDS row i * 16 + x of an A half is its row x * 8 + i; row q * 64 + j * 16 + y of B is its column
+  // q * 64 + (y / 4) * 16 + 4 j + y % 4.  A wave issues blocks q, q + 4, q + 8, q + 12 (8 rows each)
+  // of a half: in A 2 rows apart in the source, in B 8, 64 and 72 columns.
+  const int prow = wq * 8 + (lane >> 3);
+  const int chunk = (lane & 7) ^ row_key<8>(prow);
+  const uint32_t a_off = (uint32_t)((g * 128 + (prow & 15) * 8 + (prow >> 4)) * p.lda) + chunk * 16;
+  const uint32_t b_off = (uint32_t)((g * 128 + ((prow & 15) >> 2) * 16 + (prow >> 4) * 4 + (prow & 3)) * p.ldb) + chunk * 16;
+
+  f32x4 acc[RM][RN];
+  static_for<RM>([&](auto i) { static_for<RN>([&](auto j) { acc[i][j] = f32x4{}; }); });
+  int slot[2];
+  static_for<2>([&](auto u) { slot[u] = swizzled_slot<8>(x, c4 + 4 * u); });
+
+  auto dma_a = [&](int t) {
+    const int64_t k = (int64_t)t * kSB;
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(a_tile, a_span);
+    u32x4* dst = lds + (g * 2 + (t & 1)) * HALF;
+    uint32_t o = a_off;
+    asm volatile("" : "+v"(o));   // formed here, not kept in more registers
+    const bool in_k = k + chunk * 16 < K;
+    static_for<4>([&](auto i) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)(dst + (wq + 4 * i) * 64), 16,
+                                               in_k ? o + (uint32_t)(2 * i * p.lda) : kOobOffset, (int)k, 0, 0);
+    });
+  };
+  auto dma_b = [&](int t) {
+    const int64_t k = (int64_t)t * kSB;
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(b_tile, b_span);
+    u32x4* dst = lds + B0 + (t % 3) * 2 * HALF + g * HALF;
+    uint32_t o = b_off;
+    asm volatile("" : "+v"(o));
+    const bool in_k = k + chunk * 16 < K;
+    static_for<4>([&](auto i) {
+      constexpr int cols = (i & 1) * 8 + (i >> 1) * 64;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)(dst + (wq + 4 * i) * 64), 16,
+                                               in_k ? o + (uint32_t)(cols * p.ldb) : kOobOffset, (int)k, 0, 0);
+    });
+  };
+  constexpr int HELD = 2;           // A fragments read in the read phase
+  constexpr int LAG = 2;            // instructions between a sum and its addition
+  Frag<u16> fa[RM], fb[RN];
+  f32x4 sa0, sa1;
+  float sb;
+  auto read_a = [&](int t, auto i) {
+    int at = (g * 2 + (t & 1)) * HALF;
+    static_for<2>([&](auto u) { fa[i].w[u] = lds[at + slot[u] + i * 128]; });
+  };
+  auto phase_end = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    barrier_nofence();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (nk > 0) {
+    dma_a(0);
+    dma_b(0);
+    dma_b(1);
+    wait_counts<0, true>();
+    barrier_nofence();
+    if (g == 1) phase_end();
+    for (int v = 0; v < nk; ++v) {
+      {
+        const __amdgpu_buffer_rsrc_t ra = make_rsrc(sa_base + (int64_t)v * p.a_sk * 4, sa_span);
+        const __amdgpu_buffer_rsrc_t rb = make_rsrc(sb_base + (int64_t)v * p.b_sk * 4, 4);
+        sa0 = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, sa_off, 0, 0));
+        sa1 = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, sa_off + 16, 0, 0));
+        sb = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rb, 0, 0, 0));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      static_for<RN>([&](auto j) {
+        static_for<2>([&](auto u) { fb[j].w[u] = lds[B0 + (v % 3) * 2 * HALF + wq * 64 * 8 + slot[u] + j * 128]; });
+      });
+      static_for<HELD>([&](auto i) { read_a(v, i); });
+      dma_a(v + 1);
+      dma_b(v + 2);
+      wait_counts<11, true>();
+      phase_end();
+      // compute phase: the sums of an instruction are added two instructions later, when they
+      // are there
+      f32x4 t[LAG + 1];
+      float w[RM];
+      static_for<4>([&](auto i) {
+        w[i] = sa0[(int)i] * sb;
+        w[4 + i] = sa1[(int)i] * sb;
+      });
+      static_for<RM * RN + LAG>([&](auto n) {
+        if constexpr (n % RN == 0 && n / RN + HELD < RM) read_a(v, std::integral_constant<int, n / RN + HELD>{});
+        if constexpr (n < RM * RN) t[n % (LAG + 1)] = mfma_block(fb[n % RN], fa[n / RN]);
+        if constexpr (n >= LAG) {
+          constexpr int o = n - LAG, i = o / RN, j = o % RN;
+          static_for<4>([&](auto r) {
+            acc[i][j][(int)r] = __builtin_fmaf(t[o % (LAG + 1)][(int)r], w[i], acc[i][j][(int)r]);
+          });
+        }
+      });
+      static_for<RM * RN + LAG>([&](auto n) {
+        if constexpr (n % RN == 0 && n / RN + HELD < RM) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        if constexpr (n < RM * RN) __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        if constexpr (n >= LAG) __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
+      });
+      wait_counts<4, true>();
+      phase_end();
+    }
+    if (g == 0) phase_end();
+    wait_counts<0, true>();
+  }
+  store_outputs<OT, RM, RN>(p, s, acc, [&](auto i) { return s.m0 + g * 128 + x * 8 + i; }, s.n0 + wq * 64 + c4 * 16);
+}
+
 // The planes of a split k, added in order, and the epilogue.
 template <class OT>
 __global__ __launch_bounds__(256) void scaled_join(const SParams p) {
