@@ -57,21 +57,36 @@ struct STile {
   int64_t k0, k1;            // k0 a multiple of 128
 };
 
-__device__ __forceinline__ int wave_max_scan(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d, 64);
-    if (lane >= d) v = max(v, o);
-  }
+// Inclusive maximum / sum over the lanes of a wave (values >= 0), by DPP: shifts within rows of 16
+// lanes, then the last lane of a row broadcast to the rows after it.
+template <bool MAX> __device__ __forceinline__ int wave_scan(int v) {
+  auto step = [&](auto ctrl, auto rows) {
+    const int o = __builtin_amdgcn_update_dpp(0, v, decltype(ctrl)::value, decltype(rows)::value, 0xf, false);
+    v = MAX ? max(v, o) : v + o;
+  };
+  step(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xf>{});  // row_shr:1
+  step(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xf>{});
+  step(std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xf>{});
+  step(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xf>{});
+  step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});  // row_bcast:15
+  step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});  // row_bcast:31
   return v;
 }
-__device__ __forceinline__ int wave_sum_scan(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d, 64);
-    if (lane >= d) v += o;
-  }
-  return v;
+
+// 64 groups of rows, a lane each: the rows [lo, hi) of group c + lane, with the offsets clamped
+// and made non-decreasing, and the running number of tiles.  `top` is the largest offset before.
+struct GroupLane {
+  int lo, hi, tiles, upto;
+};
+template <int BM>
+__device__ __forceinline__ GroupLane group_lane(const SParams& p, int c, int lane, int top) {
+  const int M = (int)p.M, i = c + lane;
+  GroupLane r;
+  r.lo = max(wave_scan<true>(i <= p.groups ? min(max(p.offsets[i], 0), M) : 0), top);
+  r.hi = i < p.groups ? max(r.lo, min(max(p.offsets[i + 1], 0), M)) : r.lo;
+  r.tiles = (r.hi - r.lo + BM - 1) / BM * p.tiles_n;
+  r.upto = wave_scan<false>(r.tiles);
+  return r;
 }
 
 // Workgroup id -> place in the tile order: ids are dealt to the 8 XCDs in turn, and each XCD gets
@@ -106,45 +121,32 @@ __device__ __forceinline__ bool tile_share(const SParams& p, STile& s) {
   int tm = p.tiles_m, t;
   const int lane = threadIdx.x & 63;
   if (p.form == FORM_ROWS) {
-    const int G = p.groups, M = (int)p.M;
-    const int first = min(max(p.offsets[0], 0), M);
-    int total = 0, top = first;
+    const int G = p.groups;
+    int total = 0, top = 0;
+    GroupLane q;
     for (int c = 0; c < G; c += 64) {
-      const int v = c + lane < G ? min(max(p.offsets[c + lane + 1], 0), M) : 0;
-      const int hi = max(wave_max_scan(v, lane), top);
-      int lo = __shfl_up(hi, 1, 64);
-      if (lane == 0) lo = top;
-      const int n = c + lane < G ? (hi - lo + BM - 1) / BM * p.tiles_n : 0;
-      total += __shfl(wave_sum_scan(n, lane), 63, 64);
-      top = __shfl(hi, 63, 64);
+      q = group_lane<BM>(p, c, lane, top);
+      total += __builtin_amdgcn_readlane(q.upto, 63);
+      top = __builtin_amdgcn_readlane(q.hi, 63);
     }
     if ((int)blockIdx.x >= total) return false;
     t = xcd_order(blockIdx.x, total);
-    int before = 0, e = 0, lo_e = 0, hi_e = 0;
-    top = first;
+    int e = 0, group0 = 0;
+    top = 0;
     for (int c = 0; c < G; c += 64) {
-      const int v = c + lane < G ? min(max(p.offsets[c + lane + 1], 0), M) : 0;
-      const int hi = max(wave_max_scan(v, lane), top);
-      int lo = __shfl_up(hi, 1, 64);
-      if (lane == 0) lo = top;
-      const int n = c + lane < G ? (hi - lo + BM - 1) / BM * p.tiles_n : 0;
-      const int sum = wave_sum_scan(n, lane);
-      const unsigned long long past = __ballot(before + sum > t);
+      group0 = c;
+      if (G > 64) q = group_lane<BM>(p, c, lane, top);
+      const unsigned long long past = __ballot(q.upto > t);
       if (past != 0) {
-        const int l = __ffsll(past) - 1;
-        e = c + l;
-        lo_e = __shfl(lo, l, 64);
-        hi_e = __shfl(hi, l, 64);
-        t -= before + __shfl(sum - n, l, 64);
+        e = __ffsll(past) - 1;
         break;
       }
-      before += __shfl(sum, 63, 64);
-      top = __shfl(hi, 63, 64);
+      t -= __builtin_amdgcn_readlane(q.upto, 63);
+      top = __builtin_amdgcn_readlane(q.hi, 63);
     }
-    e = __builtin_amdgcn_readfirstlane(e);
-    lo_e = __builtin_amdgcn_readfirstlane(lo_e);
-    hi_e = __builtin_amdgcn_readfirstlane(hi_e);
-    t = __builtin_amdgcn_readfirstlane(t);
+    t -= __builtin_amdgcn_readlane(q.upto - q.tiles, e);
+    const int lo_e = __builtin_amdgcn_readlane(q.lo, e), hi_e = __builtin_amdgcn_readlane(q.hi, e);
+    e += group0;
     s.A += (int64_t)lo_e * p.lda;
     s.a_scale += (int64_t)lo_e * p.a_sm;
     s.B += e * p.b_l;
@@ -330,59 +332,82 @@ __global__ __launch_bounds__(256) void scaled_narrow(const SParams p, int b_bloc
 }
 
 // ------------------------------------------------------------------------------------------
-// The outputs of a lane: RM rows m, and for each of them 4 RN neighbouring columns.  Whole
-// 16-byte stores where D allows them; four lane groups cover 16 RN neighbouring columns of a row.
+// The outputs of a lane: RM rows m, and in each of them RN pieces of 4 neighbouring columns.  The
+// columns of a wave are dealt so that JP pieces of a lane make 16 bytes of D and the four lane
+// groups c4 make 64 neighbouring bytes: piece j of group c4 starts at column
+//   (j / JP) * 16 JP + c4 * 4 JP + (j % JP) * 4,
+// i.e. LDS row j * 16 + y of the wave's B tile holds that column plus y % 4, c4 = y / 4.
 // ------------------------------------------------------------------------------------------
-template <class OT, int RM, int RN, class RowOf>
-__device__ __forceinline__ void store_outputs(const SParams& p, const STile& s, f32x4 (&acc)[RM][RN],
-                                              RowOf row_of, int64_t col0) {
-  constexpr int NV = 4 * RN;                 // outputs of a lane in one row
-  constexpr int VO = 16 / (int)sizeof(OT);   // outputs in 16 bytes
-  const bool whole = col0 + NV <= p.N;
-  const bool d_vec = whole && NV % VO == 0 && p.ldd % VO == 0 && (reinterpret_cast<uintptr_t>(s.D) & 15) == 0;
-  if (p.split_k > 1) {
-    float* w = p.workspace + (int64_t)blockIdx.y * p.M * p.N;
-    static_for<RM>([&](auto i) {
-      const int64_t row = row_of(i);
-      if (row < s.M)
-        static_for<RN>([&](auto j) {
-          if (whole && p.N % 4 == 0) {
-            *reinterpret_cast<f32x4*>(w + row * p.N + col0 + 4 * j) = acc[i][j];
-          } else {
-            static_for<4>([&](auto r) {
-              if (col0 + 4 * j + r < p.N) w[row * p.N + col0 + 4 * j + r] = acc[i][j][(int)r];
-            });
-          }
+template <class OT> struct Cols {
+  static constexpr int VO = 16 / (int)sizeof(OT), JP = VO / 4;
+  __device__ static constexpr int of(int j, int c4) { return (j / JP) * 16 * JP + c4 * 4 * JP + (j % JP) * 4; }
+};
+
+// Whole 16-byte stores, no C: one straight copy of the code for each activation, because the
+// epilogue runs once a tile and its instructions are fetched anew each time.
+template <class OT, int RM, int RN, int ACT, class RowOf>
+__device__ __forceinline__ void store_whole(const SParams& p, const STile& s, f32x4 (&acc)[RM][RN], RowOf row_of,
+                                            int64_t col0, int x, int c4) {
+  typedef Cols<OT> CM;
+  constexpr int VO = CM::VO, NQ = RN / CM::JP;
+  alignas(16) OT bias[NQ][VO];
+  static_for<NQ>([&](auto q) {
+    u32x4 w = {0, 0, 0, 0};
+    if (p.bias) w = *reinterpret_cast<const u32x4*>((const OT*)p.bias + col0 + CM::of(q * CM::JP, c4));
+    *reinterpret_cast<u32x4*>(bias[q]) = w;
+  });
+  static_for<RM>([&](auto i) {
+    const int64_t row = row_of(i, x);
+    if (row < s.M) {
+      const float rs = s.row_scale ? s.row_scale[row] : 1.f;
+      OT* d = (OT*)s.D + row * p.ldd + col0 + CM::of(0, c4);
+      static_for<NQ>([&](auto q) {
+        alignas(16) OT o[VO];
+        static_for<VO>([&](auto c) {
+          float v = acc[i][q * CM::JP + c / 4][c % 4] * p.alpha * rs;
+          v += SOut<OT>::load(bias[q], c);
+          o[c] = SOut<OT>::bits(ACT == 1 ? relu(v) : ACT == 2 ? gelu(v) : ACT == 3 ? silu(v) : v);
         });
-    });
+        *reinterpret_cast<u32x4*>(d + CM::of(q * CM::JP, 0)) = *reinterpret_cast<const u32x4*>(o);
+      });
+    }
+  });
+}
+
+// The outputs of a workgroup with BN columns: col0 is the wave's first column, row_of(i, x) the row
+// of row block i in lane x = lane % 16.  `lds` is the kernel's LDS, at least 16 x 68 floats a wave.
+template <class OT, int BN, int RM, int RN, class RowOf>
+__device__ __forceinline__ void store_outputs(const SParams& p, const STile& s, f32x4 (&acc)[RM][RN],
+                                              RowOf row_of, int64_t col0, u32x4* lds, int wave) {
+  typedef Cols<OT> CM;
+  const int lane = threadIdx.x & 63, x = lane & 15, c4 = lane >> 4;
+  if (s.n0 + BN <= p.N && !s.C && p.split_k <= 1 && p.ldd % CM::VO == 0 &&
+      ((reinterpret_cast<uintptr_t>(s.D) | reinterpret_cast<uintptr_t>(p.bias)) & 15) == 0) {
+    if (p.act == 0) store_whole<OT, RM, RN, 0>(p, s, acc, row_of, col0, x, c4);
+    else if (p.act == 3) store_whole<OT, RM, RN, 3>(p, s, acc, row_of, col0, x, c4);
+    else if (p.act == 2) store_whole<OT, RM, RN, 2>(p, s, acc, row_of, col0, x, c4);
+    else store_whole<OT, RM, RN, 1>(p, s, acc, row_of, col0, x, c4);
     return;
   }
-  float bias[NV];
-  static_for<NV>([&](auto c) { bias[c] = p.bias && col0 + c < p.N ? SOut<OT>::load(p.bias, col0 + c) : 0.f; });
+  // everything else element by element, a row block of the wave at a time through LDS, so that
+  // the code is a short loop and a row's neighbours are stored together
+  constexpr int W = 16 * RN, PITCH = W + 4;
+  static_assert(W == 64, "a lane for each column");
+  float* mine = reinterpret_cast<float*>(lds) + wave * 16 * PITCH;
+  __syncthreads();              // the operands in LDS have been read
+  const int64_t col = col0 + lane;
   static_for<RM>([&](auto i) {
-    const int64_t row = row_of(i);
-    if (row < s.M) {
-      const float a = p.alpha, rs = s.row_scale ? s.row_scale[row] : 1.f;
-      float v[NV];
-      static_for<NV>([&](auto c) { v[c] = acc[i][c / 4][c % 4] * a * rs; });
-      if (s.C) static_for<NV>([&](auto c) {
-        if (col0 + c < p.N) v[c] += p.beta * SOut<OT>::load(s.C, row * p.ldc + col0 + c);
-      });
-      static_for<NV>([&](auto c) { v[c] += bias[c]; });
-      if (p.act == 2) static_for<NV>([&](auto c) { v[c] = gelu(v[c]); });
-      else if (p.act == 1) static_for<NV>([&](auto c) { v[c] = relu(v[c]); });
-      else if (p.act == 3) static_for<NV>([&](auto c) { v[c] = silu(v[c]); });
-      OT* d = (OT*)s.D + row * p.ldd + col0;
-      if (d_vec) {
-        static_for<(NV + VO - 1) / VO>([&](auto q) {
-          OT o[VO];
-          static_for<VO>([&](auto c) { o[c] = SOut<OT>::bits(v[(q * VO + c) % NV]); });
-          *reinterpret_cast<u32x4*>(d + q * VO) = *reinterpret_cast<const u32x4*>(o);
-        });
-      } else {
-        static_for<NV>([&](auto c) { if (col0 + c < p.N) d[(int)c] = SOut<OT>::bits(v[c]); });
-      }
+    static_for<RN>([&](auto j) { *reinterpret_cast<f32x4*>(&mine[x * PITCH + CM::of(j, c4)]) = acc[i][j]; });
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll 1
+    for (int r = 0; r < 16; ++r) {
+      const int64_t row = row_of(i, r);
+      if (row >= s.M || col >= p.N) continue;
+      const float v = mine[r * PITCH + lane];
+      if (p.split_k > 1) p.workspace[((int64_t)blockIdx.y * p.M + row) * p.N + col] = v;
+      else finish_one<OT>(p, s, row, col, v);
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   });
 }
 
@@ -394,9 +419,8 @@ typedef __attribute__((address_space(1))) const void gbl_void_t;
 // chunks) and their BM + BN scales, fetched by 4-byte DMA so that scales may have any strides.
 //
 // Rows are placed in LDS so that a lane's rows are neighbours: LDS row i * 16 + x of a wave's A
-// tile is its row x * RM + i, and LDS row j * 16 + y of its B tile is its row
-// (y / 4) * 4 RN + 4 j + y % 4.  The lane's A scales (and per-column B scales) are then
-// contiguous in LDS, and its outputs in D.  The placement costs nothing: every DMA lane has its
+// tile is its row x * RM + i, and LDS row j * 16 + y of its B tile the column that Cols gives.  The
+// lane's A scales are then contiguous in LDS, and its outputs in D.  The placement costs nothing: every DMA lane has its
 // own source address.
 // ------------------------------------------------------------------------------------------
 template <int BM, int BN, int WM, int WN, int ST, int BB, class OT, int OCC>
@@ -435,7 +459,7 @@ __global__ __launch_bounds__(WM * WN * 64, OCC) void scaled_tile(const SParams p
       off[i] = (uint32_t)((w * TM + (q & 15) * RM + (q >> 4)) * p.lda) + chunk * 16;
     } else {
       const int w = (R - BM) / TN, q = (R - BM) % TN, y = q & 15;
-      off[i] = (uint32_t)((w * TN + (y >> 2) * (4 * RN) + (q >> 4) * 4 + (y & 3)) * p.ldb) + chunk * 16;
+      off[i] = (uint32_t)((w * TN + Cols<OT>::of(q >> 4, y >> 2) + (y & 3)) * p.ldb) + chunk * 16;
     }
   });
   static_assert(NW % 2 == 0, "the row key of a wave's DMA blocks is the same in all of them");
@@ -492,7 +516,7 @@ __global__ __launch_bounds__(WM * WN * 64, OCC) void scaled_tile(const SParams p
     static_for<RM>([&](auto i) { sa[i] = ls[wm * TM + x * RM + i]; });
     f32x4 sb[BB == 1 ? RN : 1];
     if constexpr (BB == 1) {
-      static_for<RN>([&](auto j) { sb[j] = *reinterpret_cast<const f32x4*>(&ls[BM + wn * TN + g * 4 * RN + 4 * j]); });
+      static_for<RN>([&](auto j) { sb[j] = *reinterpret_cast<const f32x4*>(&ls[BM + wn * TN + Cols<OT>::of(j, g)]); });
     } else {
       const float one = ls[BM + wn * TN];
       static_for<RM>([&](auto i) { sa[i] *= one; });
@@ -527,8 +551,8 @@ __global__ __launch_bounds__(WM * WN * 64, OCC) void scaled_tile(const SParams p
     }
     wait_counts<0, true>();  // zero blocks issued past the end
   }
-  store_outputs<OT, RM, RN>(p, s, acc, [&](auto i) { return s.m0 + wm * TM + x * RM + i; },
-                            s.n0 + wn * TN + g * 4 * RN);
+  store_outputs<OT, BN, RM, RN>(p, s, acc, [&](int i, int r) { return s.m0 + wm * TM + r * RM + i; },
+                                s.n0 + wn * TN, lds, wave);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -689,13 +713,13 @@ __global__ __launch_bounds__(512, 1) void scaled_pp(const SParams p) {
   const int64_t sa_span = uniform_i64((s.M - s.m0) * 4);
   const uint32_t sa_off = (uint32_t)(g * 128 + x * 8) * 4;
 
-  // LDS row i * 16 + x of an A half is its row x * 8 + i; row q * 64 + j * 16 + y of B is its column
-  // q * 64 + (y / 4) * 16 + 4 j + y % 4.  A wave issues blocks q, q + 4, q + 8, q + 12 (8 rows each)
-  // of a half: in A 2 rows apart in the source, in B 8, 64 and 72 columns.
+  // LDS row i * 16 + x of an A half is its row x * 8 + i; row q * 64 + j * 16 + y of B the column of
+  // Cols.  A wave issues blocks q, q + 4, q + 8, q + 12 (8 rows each) of a half: in A 2 rows apart in
+  // the source, in B 32, 64 and 96 columns.
   const int prow = wq * 8 + (lane >> 3);
   const int chunk = (lane & 7) ^ row_key<8>(prow);
   const uint32_t a_off = (uint32_t)((g * 128 + (prow & 15) * 8 + (prow >> 4)) * p.lda) + chunk * 16;
-  const uint32_t b_off = (uint32_t)((g * 128 + ((prow & 15) >> 2) * 16 + (prow >> 4) * 4 + (prow & 3)) * p.ldb) + chunk * 16;
+  const uint32_t b_off = (uint32_t)((g * 128 + Cols<OT>::of(prow >> 4, (prow & 15) >> 2) + (prow & 3)) * p.ldb) + chunk * 16;
 
   f32x4 acc[RM][RN];
   static_for<RM>([&](auto i) { static_for<RN>([&](auto j) { acc[i][j] = f32x4{}; }); });
@@ -722,7 +746,7 @@ __global__ __launch_bounds__(512, 1) void scaled_pp(const SParams p) {
     asm volatile("" : "+v"(o));
     const bool in_k = k + chunk * 16 < K;
     static_for<4>([&](auto i) {
-      constexpr int cols = (i & 1) * 8 + (i >> 1) * 64;
+      constexpr int cols = Cols<OT>::of(2 * (i & 1), 0) + (i >> 1) * 64;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)(dst + (wq + 4 * i) * 64), 16,
                                                in_k ? o + (uint32_t)(cols * p.ldb) : kOobOffset, (int)k, 0, 0);
     });
@@ -765,8 +789,9 @@ __global__ __launch_bounds__(512, 1) void scaled_pp(const SParams p) {
       dma_b(v + 2);
       wait_counts<11, true>();
       phase_end();
-      // compute phase: the sums of an instruction are added two instructions later, when they
-      // are there
+      // compute phase: the sums of an instruction are added LAG instructions later, when they are
+      // there; the wave is preferred to the one that reads
+      __builtin_amdgcn_s_setprio(1);
       f32x4 t[LAG + 1];
       float w[RM];
       static_for<4>([&](auto i) {
@@ -788,13 +813,15 @@ __global__ __launch_bounds__(512, 1) void scaled_pp(const SParams p) {
         if constexpr (n < RM * RN) __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
         if constexpr (n >= LAG) __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
       });
+      __builtin_amdgcn_s_setprio(0);
       wait_counts<4, true>();
       phase_end();
     }
     if (g == 0) phase_end();
     wait_counts<0, true>();
   }
-  store_outputs<OT, RM, RN>(p, s, acc, [&](auto i) { return s.m0 + g * 128 + x * 8 + i; }, s.n0 + wq * 64 + c4 * 16);
+  store_outputs<OT, BN, RM, RN>(p, s, acc, [&](int i, int r) { return s.m0 + g * 128 + r * 8 + i; },
+                                s.n0 + wq * 64, lds, wave);
 }
 
 // The planes of a split k, added in order, and the epilogue.
