@@ -343,30 +343,41 @@ template <class OT> struct Cols {
   __device__ static constexpr int of(int j, int c4) { return (j / JP) * 16 * JP + c4 * 4 * JP + (j % JP) * 4; }
 };
 
-// Whole 16-byte stores, no C: one straight copy of the code for each activation, because the
-// epilogue runs once a tile and its instructions are fetched anew each time.
-template <class OT, int RM, int RN, int ACT, class RowOf>
+// Whole 16-byte loads of C and stores of D: one straight copy of the code for each activation and
+// for C or none, because the epilogue runs once a tile and its instructions are fetched anew each
+// time.  All of a lane's C is loaded first (D may be C, so no load could pass a store).
+template <class OT, int RM, int RN, int ACT, bool HAS_C, class RowOf>
 __device__ __forceinline__ void store_whole(const SParams& p, const STile& s, f32x4 (&acc)[RM][RN], RowOf row_of,
                                             int64_t col0, int x, int c4) {
   typedef Cols<OT> CM;
   constexpr int VO = CM::VO, NQ = RN / CM::JP;
-  alignas(16) OT bias[NQ][VO];
+  const int64_t col = col0 + CM::of(0, c4);
+  u32x4 bias[NQ], c[HAS_C ? RM : 1][NQ];
+  if constexpr (HAS_C) {
+    static_for<RM>([&](auto i) {
+      const int64_t row = row_of(i, x);
+      static_for<NQ>([&](auto q) {
+        c[i][q] = u32x4{0, 0, 0, 0};
+        if (row < s.M) c[i][q] = *reinterpret_cast<const u32x4*>((const OT*)s.C + row * p.ldc + col + CM::of(q * CM::JP, 0));
+      });
+    });
+  }
   static_for<NQ>([&](auto q) {
-    u32x4 w = {0, 0, 0, 0};
-    if (p.bias) w = *reinterpret_cast<const u32x4*>((const OT*)p.bias + col0 + CM::of(q * CM::JP, c4));
-    *reinterpret_cast<u32x4*>(bias[q]) = w;
+    bias[q] = u32x4{0, 0, 0, 0};
+    if (p.bias) bias[q] = *reinterpret_cast<const u32x4*>((const OT*)p.bias + col + CM::of(q * CM::JP, 0));
   });
   static_for<RM>([&](auto i) {
     const int64_t row = row_of(i, x);
     if (row < s.M) {
       const float rs = s.row_scale ? s.row_scale[row] : 1.f;
-      OT* d = (OT*)s.D + row * p.ldd + col0 + CM::of(0, c4);
+      OT* d = (OT*)s.D + row * p.ldd + col;
       static_for<NQ>([&](auto q) {
         alignas(16) OT o[VO];
-        static_for<VO>([&](auto c) {
-          float v = acc[i][q * CM::JP + c / 4][c % 4] * p.alpha * rs;
-          v += SOut<OT>::load(bias[q], c);
-          o[c] = SOut<OT>::bits(ACT == 1 ? relu(v) : ACT == 2 ? gelu(v) : ACT == 3 ? silu(v) : v);
+        static_for<VO>([&](auto e) {
+          float v = acc[i][q * CM::JP + e / 4][e % 4] * p.alpha * rs;
+          if constexpr (HAS_C) v += p.beta * SOut<OT>::load(&c[i][q], e);
+          v += SOut<OT>::load(&bias[q], e);
+          o[e] = SOut<OT>::bits(ACT == 1 ? relu(v) : ACT == 2 ? gelu(v) : ACT == 3 ? silu(v) : v);
         });
         *reinterpret_cast<u32x4*>(d + CM::of(q * CM::JP, 0)) = *reinterpret_cast<const u32x4*>(o);
       });
@@ -381,12 +392,17 @@ __device__ __forceinline__ void store_outputs(const SParams& p, const STile& s, 
                                               RowOf row_of, int64_t col0, u32x4* lds, int wave) {
   typedef Cols<OT> CM;
   const int lane = threadIdx.x & 63, x = lane & 15, c4 = lane >> 4;
-  if (s.n0 + BN <= p.N && !s.C && p.split_k <= 1 && p.ldd % CM::VO == 0 &&
+  const bool c_ok = !s.C || (p.ldc % CM::VO == 0 && (reinterpret_cast<uintptr_t>(s.C) & 15) == 0);
+  if (s.n0 + BN <= p.N && c_ok && p.split_k <= 1 && p.ldd % CM::VO == 0 &&
       ((reinterpret_cast<uintptr_t>(s.D) | reinterpret_cast<uintptr_t>(p.bias)) & 15) == 0) {
-    if (p.act == 0) store_whole<OT, RM, RN, 0>(p, s, acc, row_of, col0, x, c4);
-    else if (p.act == 3) store_whole<OT, RM, RN, 3>(p, s, acc, row_of, col0, x, c4);
-    else if (p.act == 2) store_whole<OT, RM, RN, 2>(p, s, acc, row_of, col0, x, c4);
-    else store_whole<OT, RM, RN, 1>(p, s, acc, row_of, col0, x, c4);
+    auto whole = [&](auto act) {
+      if (s.C) store_whole<OT, RM, RN, decltype(act)::value, true>(p, s, acc, row_of, col0, x, c4);
+      else store_whole<OT, RM, RN, decltype(act)::value, false>(p, s, acc, row_of, col0, x, c4);
+    };
+    if (p.act == 0) whole(std::integral_constant<int, 0>{});
+    else if (p.act == 3) whole(std::integral_constant<int, 3>{});
+    else if (p.act == 2) whole(std::integral_constant<int, 2>{});
+    else whole(std::integral_constant<int, 1>{});
     return;
   }
   // everything else element by element, a row block of the wave at a time through LDS, so that

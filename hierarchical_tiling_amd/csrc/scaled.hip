@@ -51,7 +51,7 @@ hipError_t go_pp(const SParams& p, dim3 grid, hipStream_t s) {
    {{&go_stream<RM, NBW, WK, R, OCC, 128, u16>, &go_stream<RM, NBW, WK, R, OCC, 128, float>},     \
     {&go_stream<RM, NBW, WK, R, OCC, 1, u16>, &go_stream<RM, NBW, WK, R, OCC, 1, float>}}}
 
-enum { V_NARROW, V_S16, V_S16N, V_S32, V_S64, V_T64, V_T128, V_T256, V_PP, V_COUNT };
+enum { V_NARROW, V_S16, V_S16N, V_S32, V_S64, V_T64, V_T128, V_PP, V_COUNT };
 const Variant kVariants[V_COUNT] = {
     {"narrow_64x64", 64, 64, 4, 16384, 0,
      {{&go_narrow<128, u16>, &go_narrow<128, float>}, {&go_narrow<1, u16>, &go_narrow<1, float>}}},
@@ -61,7 +61,6 @@ const Variant kVariants[V_COUNT] = {
     HT_STREAM("stream_64x32_w4", 4, 2, 4, 3, 1),
     HT_TILE("tile_64x128_w2x2", 64, 128, 2, 2, 3, 2),
     HT_TILE("tile_128x128_w2x2", 128, 128, 2, 2, 2, 2),
-    HT_TILE("tile_256x256_w2x4", 256, 256, 2, 4, 2, 1),
     {"pingpong_256x256", 256, 256, 8, 160 * 1024, 0, {{&go_pp, nullptr}, {nullptr, nullptr}}},
 };
 
@@ -103,8 +102,9 @@ void choose(gemm_scaled_s* h) {
   if (rows <= 16) h->variant = up(d.N, 32) * row_tiles(*h, 16) * many >= kCUs ? V_S16 : V_S16N;
   else if (rows <= 32) h->variant = V_S32;
   else if (rows <= 64) h->variant = V_S64;
-  else if (up(d.N, 256) * row_tiles(*h, 256) * many >= kCUs && rows > 128 && d.d_type == GEMM_BF16)
-    h->variant = d.b_block == kSB && d.a_scale_m == 1 ? V_PP : V_T256;
+  else if (up(d.N, 256) * row_tiles(*h, 256) * many >= kCUs && rows > 128 && d.d_type == GEMM_BF16 &&
+           d.b_block == kSB && d.a_scale_m == 1)
+    h->variant = V_PP;
   else if (up(d.N, 128) * row_tiles(*h, 128) * many >= kCUs) h->variant = V_T128;
   else h->variant = V_T64;
   const Variant& v = kVariants[h->variant];
