@@ -439,7 +439,7 @@ typedef __attribute__((address_space(1))) const void gbl_void_t;
 // lane's A scales are then contiguous in LDS, and its outputs in D.  The placement costs nothing: every DMA lane has its
 // own source address.
 // ------------------------------------------------------------------------------------------
-template <int BM, int BN, int WM, int WN, int ST, int BB, class OT, int OCC>
+template <int BM, int BN, int WM, int WN, int ST, int BB, class OT, int OCC, bool PIPE>
 __global__ __launch_bounds__(WM * WN * 64, OCC) void scaled_tile(const SParams p) {
   constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, RM = TM / 16, RN = TN / 16;
   constexpr int OPS_T = (BM + BN) / 8 / NW;          // tile DMA instructions per wave and block
@@ -521,49 +521,84 @@ __global__ __launch_bounds__(WM * WN * 64, OCC) void scaled_tile(const SParams p
   int slot[2];
   static_for<2>([&](auto u) { slot[u] = swizzled_slot<8>(x, g + 4 * u); });
 
-  auto compute = [&](int stage) {
+  // what a wave reads of a block: fragments and scales (a 128-wide B scale is in the A scales)
+  struct Held {
+    Frag<OT> fa[PIPE ? RM : 1], fb[RN];
+    float sa[RM];
+    f32x4 sb[BB == 1 ? RN : 1];
+  };
+  auto read_a = [&](int stage, Frag<OT>& f, int i) {
+    const u32x4* la = lds + stage * STAGE + wm * TM * 8;
+    static_for<2>([&](auto u) { f.set(u, la[i * 128 + slot[u]]); });
+  };
+  auto read = [&](int stage, Held& h) {
     const u32x4* st = lds + stage * STAGE;
-    const u32x4* la = st + wm * TM * 8;
     const u32x4* lb = st + (BM + wn * TN) * 8;
     const float* ls = reinterpret_cast<const float*>(st + (BM + BN) * 8);
-    Frag<OT> fb[RN];
-    static_for<RN>([&](auto j) { static_for<2>([&](auto u) { fb[j].set(u, lb[j * 128 + slot[u]]); }); });
-    float sa[RM];
-    static_for<RM>([&](auto i) { sa[i] = ls[wm * TM + x * RM + i]; });
-    f32x4 sb[BB == 1 ? RN : 1];
+    static_for<RN>([&](auto j) { static_for<2>([&](auto u) { h.fb[j].set(u, lb[j * 128 + slot[u]]); }); });
+    if constexpr (PIPE) static_for<RM>([&](auto i) { read_a(stage, h.fa[i], i); });
+    static_for<RM>([&](auto i) { h.sa[i] = ls[wm * TM + x * RM + i]; });
     if constexpr (BB == 1) {
-      static_for<RN>([&](auto j) { sb[j] = *reinterpret_cast<const f32x4*>(&ls[BM + wn * TN + Cols<OT>::of(j, g)]); });
+      static_for<RN>([&](auto j) { h.sb[j] = *reinterpret_cast<const f32x4*>(&ls[BM + wn * TN + Cols<OT>::of(j, g)]); });
     } else {
       const float one = ls[BM + wn * TN];
-      static_for<RM>([&](auto i) { sa[i] *= one; });
+      static_for<RM>([&](auto i) { h.sa[i] *= one; });
     }
+  };
+  auto compute = [&](int stage, Held& h) {
     static_for<RM>([&](auto i) {
-      Frag<OT> fa;
-      static_for<2>([&](auto u) { fa.set(u, la[i * 128 + slot[u]]); });
+      if constexpr (!PIPE) read_a(stage, h.fa[0], i);
       f32x4 t[RN];
-      static_for<RN>([&](auto j) { t[j] = mfma_block(fb[j], fa); });
+      static_for<RN>([&](auto j) { t[j] = mfma_block(h.fb[j], h.fa[PIPE ? (int)i : 0]); });
       static_for<RN>([&](auto j) {
         static_for<4>([&](auto r) {
-          const float w = BB == 1 ? sa[i] * sb[BB == 1 ? (int)j : 0][(int)r] : sa[i];
+          const float w = BB == 1 ? h.sa[i] * h.sb[BB == 1 ? (int)j : 0][(int)r] : h.sa[i];
           acc[i][j][(int)r] = __builtin_fmaf(t[j][(int)r], w, acc[i][j][(int)r]);
         });
       });
     });
   };
-
+  // Block t + 1 has landed for this wave and, behind the barrier, for all; and all are done with
+  // the stage that is refilled next.
+  auto turn = [&]() {
+    wait_counts<(ST - 2) * OPS, true>();
+    barrier_nofence();
+  };
   if (nk > 0) {
-    static_for<ST - 1>([&](auto q) { dma(q, q); });
-    int stage = 0;
-    for (int t = 0; t < nk; ++t) {
-      // block t has landed for this wave and, behind the barrier, for all; the stage refilled
-      // next was last read before it
-      wait_counts<(ST - 2) * OPS, true>();
+    if constexpr (PIPE) {
+      // A block's fragments are read into registers one block ahead of its matrix instructions, so
+      // that no LDS round trip stands in front of them; its stage is then free.
+      static_for<ST>([&](auto q) { dma(q, q); });
+      wait_counts<(ST - 1) * OPS, true>();
       barrier_nofence();
-      int next = stage + ST - 1;
-      if (next >= ST) next -= ST;
-      dma(t + ST - 1, next);
-      compute(stage);
-      if (++stage == ST) stage = 0;
+      Held h[2];
+      read(0, h[0]);
+      int stage = 0;               // of block t
+      auto step = [&](int t, Held& now, Held& next) {
+        turn();
+        dma(t + ST, stage);
+        if (++stage == ST) stage = 0;
+        if (t + 1 < nk) read(stage, next);
+        compute(0, now);
+      };
+      for (int t = 0; t < nk; t += 2) {
+        step(t, h[0], h[1]);
+        if (t + 1 >= nk) break;
+        step(t + 1, h[1], h[0]);
+      }
+    } else {
+      static_for<ST - 1>([&](auto q) { dma(q, q); });
+      int stage = 0;
+      for (int t = 0; t < nk; ++t) {
+        turn();
+        int next = stage + ST - 1;
+        if (next >= ST) next -= ST;
+        dma(t + ST - 1, next);
+        Held h;
+        read(stage, h);
+        compute(stage, h);
+        if (++stage == ST) stage = 0;
+      }
     }
     wait_counts<0, true>();  // zero blocks issued past the end
   }

@@ -24,7 +24,8 @@ struct Variant {
 
 template <int BM, int BN, int WM, int WN, int ST, int OCC, int BB, class OT>
 hipError_t go_tile(const SParams& p, dim3 grid, hipStream_t s) {
-  hipLaunchKernelGGL((scaled_tile<BM, BN, WM, WN, ST, BB, OT, OCC>), grid, dim3(WM * WN * 64), 0, s, p);
+  constexpr bool pipe = sizeof(OT) == 2;
+  hipLaunchKernelGGL((scaled_tile<BM, BN, WM, WN, ST, BB, OT, OCC, pipe>), grid, dim3(WM * WN * 64), 0, s, p);
   return hipGetLastError();
 }
 template <int RM, int NBW, int WK, int R, int OCC, int BB, class OT>

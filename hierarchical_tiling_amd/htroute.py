@@ -6,8 +6,8 @@ from __future__ import annotations
 import ctypes
 
 from . import htgemm
-from .htgemm import GEMM_ERR_INVALID_ARG, GemmError, _addr, _check, _stream
-from .htscaled import type_code
+from .htgemm import GEMM_ERR_INVALID_ARG, GemmError, _check
+from .htscaled import _stream, type_code
 
 _i32, _i64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
 
@@ -58,77 +58,105 @@ def workspace_size(tokens, topk, experts) -> int:
     return n.value
 
 
-def _require(ok, what):
-    if not ok:
-        raise GemmError(GEMM_ERR_INVALID_ARG, what)
+def _bad(what):
+    return GemmError(GEMM_ERR_INVALID_ARG, what)
 
 
-def _whole(t, dtype, n, what):
-    """A contiguous tensor of `n` values of a type, or None."""
-    _require(t is None or (t.dtype == dtype and t.numel() == n and t.is_contiguous()), what)
+def _is(t, dtype, n):
+    """Whether t is a contiguous tensor of n values of a type."""
+    return t.dtype is dtype and t.numel() == n and t.is_contiguous()
+
+
+def _mask(mask, tokens, what):
+    """Address of a mask of a byte for each token, or None."""
+    if mask is None:
+        return None
+    if mask.element_size() != 1 or mask.numel() != tokens or not mask.is_contiguous():
+        raise _bad(what)
+    return mask.data_ptr()
 
 
 def _room(workspace, tokens, topk, experts, what):
-    _require(workspace is not None and
-             workspace.numel() * workspace.element_size() >= workspace_size(tokens, topk, experts), what)
+    """Address of a workspace of the size these need."""
+    if workspace is None:
+        raise _bad(what)
+    n = ctypes.c_size_t()
+    rc = (_lib or lib()).route_workspace_size(tokens, topk, experts, ctypes.byref(n))
+    if rc or workspace.numel() * workspace.element_size() < n.value:
+        raise GemmError(rc or GEMM_ERR_INVALID_ARG, what)
+    return workspace.data_ptr()
+
+
+def _types():
+    global _i32t, _f32t
+    import torch
+    _i32t, _f32t = torch.int32, torch.float32
+
+
+_i32t = _f32t = None
 
 
 def route(ids, counts, offsets, order=None, slot=None, mask=None, align=1, workspace=None, stream=None):
     """route_experts: ids (tokens, topk) int32 to counts (experts), offsets (experts + 1), order (at
     least tokens * topk + experts * (align - 1)) and slot (tokens, topk), all int32."""
-    import torch
-    what, i32 = "route", torch.int32
-    _require(ids.dim() == 2 and ids.dtype == i32 and (ids.stride(1) == 1 or ids.shape[1] == 1), what)
+    if _i32t is None:
+        _types()
+    if ids.dim() != 2 or ids.dtype is not _i32t:
+        raise _bad("route")
     tokens, topk = ids.shape
+    step, one = ids.stride()
     experts = counts.numel()
-    _whole(counts, i32, experts, what)
-    _whole(offsets, i32, experts + 1, what)
-    _whole(slot, i32, tokens * topk, what)
-    _whole(order, i32, 0 if order is None else order.numel(), what)
-    _require(mask is None or (mask.element_size() == 1 and mask.numel() == tokens and mask.is_contiguous()), what)
-    _room(workspace, tokens, topk, experts, what)
-    a = route_args(ids.data_ptr(), _addr(mask), tokens, max(ids.stride(0), topk), topk, experts, align,
-                   counts.data_ptr(), offsets.data_ptr(), _addr(order), 0 if order is None else order.numel(),
-                   _addr(slot), workspace.data_ptr())
-    _check(lib().route_experts(ctypes.byref(a), _stream(stream)), "route_experts")
+    rows = 0 if order is None else order.numel()
+    if ((one != 1 and topk > 1) or not _is(counts, _i32t, experts) or not _is(offsets, _i32t, experts + 1) or
+            (slot is not None and not _is(slot, _i32t, tokens * topk)) or
+            (order is not None and not _is(order, _i32t, rows))):
+        raise _bad("route")
+    a = route_args(ids.data_ptr(), _mask(mask, tokens, "route"), tokens, step if step > topk else topk, topk, experts,
+                   align, counts.data_ptr(), offsets.data_ptr(), None if order is None else order.data_ptr(), rows,
+                   None if slot is None else slot.data_ptr(), _room(workspace, tokens, topk, experts, "route"))
+    rc = _lib.route_experts(ctypes.byref(a), _stream(stream))
+    if rc:
+        raise GemmError(rc, "route_experts")
 
 
-def _logits(logits, counts, mask, what):
-    import torch
-    _require(logits.dim() == 2 and (logits.stride(1) == 1 or logits.shape[1] == 1), what)
+def _logits(logits, counts, what):
+    if _i32t is None:
+        _types()
+    if logits.dim() != 2:
+        raise _bad(what)
     tokens, experts = logits.shape
-    _whole(counts, torch.int32, experts, what)
-    _require(mask is None or (mask.element_size() == 1 and mask.numel() == tokens and mask.is_contiguous()), what)
-    return tokens, experts
+    step, one = logits.stride()
+    if (one != 1 and experts > 1) or not _is(counts, _i32t, experts):
+        raise _bad(what)
+    return tokens, experts, step if step > experts else experts
 
 
 def balance_loss(logits, counts, topk, loss, prob, live, mask=None, coef=1.0, workspace=None, stream=None):
     """balance_loss: logits (tokens, experts) and the routing's counts to loss (1), prob (experts)
     and live (1)."""
-    import torch
-    what = "balance_loss"
-    tokens, experts = _logits(logits, counts, mask, what)
-    _whole(loss, torch.float32, 1, what)
-    _whole(prob, torch.float32, experts, what)
-    _whole(live, torch.int32, 1, what)
-    _room(workspace, tokens, topk, experts, what)
-    a = balance_args(logits.data_ptr(), type_code(logits), experts, topk, coef, tokens,
-                     max(logits.stride(0), experts), _addr(mask), counts.data_ptr(), loss.data_ptr(),
-                     prob.data_ptr(), live.data_ptr(), workspace.data_ptr())
-    _check(lib().balance_loss(ctypes.byref(a), _stream(stream)), "balance_loss")
+    tokens, experts, ld = _logits(logits, counts, "balance_loss")
+    if not (_is(loss, _f32t, 1) and _is(prob, _f32t, experts) and _is(live, _i32t, 1)):
+        raise _bad("balance_loss")
+    a = balance_args(logits.data_ptr(), type_code(logits), experts, topk, coef, tokens, ld,
+                     _mask(mask, tokens, "balance_loss"), counts.data_ptr(), loss.data_ptr(), prob.data_ptr(),
+                     live.data_ptr(), _room(workspace, tokens, topk, experts, "balance_loss"))
+    rc = _lib.balance_loss(ctypes.byref(a), _stream(stream))
+    if rc:
+        raise GemmError(rc, "balance_loss")
 
 
 def balance_grad(logits, counts, topk, live, d_loss, d_logits, mask=None, coef=1.0, stream=None):
     """balance_grad: the loss's gradient with respect to the logits, d_loss (1) times it, into
     d_logits (the logits' shape and type)."""
-    import torch
-    what = "balance_grad"
-    tokens, experts = _logits(logits, counts, mask, what)
-    _whole(live, torch.int32, 1, what)
-    _whole(d_loss, torch.float32, 1, what)
-    _require(d_logits.shape == logits.shape and d_logits.dtype == logits.dtype and
-             (d_logits.stride(1) == 1 or experts == 1), what)
-    a = balance_grad_args(logits.data_ptr(), type_code(logits), experts, topk, coef, tokens,
-                          max(logits.stride(0), experts), _addr(mask), counts.data_ptr(), live.data_ptr(),
-                          d_loss.data_ptr(), d_logits.data_ptr(), max(d_logits.stride(0), experts))
-    _check(lib().balance_grad(ctypes.byref(a), _stream(stream)), "balance_grad")
+    tokens, experts, ld = _logits(logits, counts, "balance_grad")
+    if d_logits.shape != logits.shape or d_logits.dtype is not logits.dtype:
+        raise _bad("balance_grad")
+    step, one = d_logits.stride()
+    if (one != 1 and experts > 1) or not (_is(live, _i32t, 1) and _is(d_loss, _f32t, 1)):
+        raise _bad("balance_grad")
+    a = balance_grad_args(logits.data_ptr(), type_code(logits), experts, topk, coef, tokens, ld,
+                          _mask(mask, tokens, "balance_grad"), counts.data_ptr(), live.data_ptr(), d_loss.data_ptr(),
+                          d_logits.data_ptr(), step if step > experts else experts)
+    rc = (_lib or lib()).balance_grad(ctypes.byref(a), _stream(stream))
+    if rc:
+        raise GemmError(rc, "balance_grad")

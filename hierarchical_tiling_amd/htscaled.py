@@ -7,7 +7,8 @@ from __future__ import annotations
 import ctypes
 
 from . import htgemm
-from .htgemm import ACTS, DTYPES, GEMM_ERR_INVALID_ARG, GemmError, _addr, _check, _stream
+from .htgemm import ACTS, DTYPES, GEMM_ERR_INVALID_ARG, GemmError, _addr, _check
+from .htgemm import _stream as _stream_of
 
 FORMS = {"single": 0, "batch": 1, "rows": 2, "k": 3}
 _i32, _i64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
@@ -45,6 +46,22 @@ class quant_args(ctypes.Structure):
 EXPORTED = ["gemm_scaled_create", "gemm_scaled_workspace_size", "gemm_scaled_run", "gemm_scaled_get_info",
             "gemm_scaled_destroy", "quant_blocks"]
 _lib = None
+
+
+def _stream(s):
+    """The hipStream_t of `s`, or of torch's current stream: as htgemm's, by the shorter way to the
+    raw handle, since these calls are made many times a layer."""
+    if s is not None:
+        return _stream_of(s)
+    global _raw_stream, _device
+    if _raw_stream is None:
+        import torch
+        torch.cuda.current_stream()      # initialises the runtime if nothing has
+        _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    return _raw_stream(_device())
+
+
+_raw_stream = _device = None
 
 
 def lib():
@@ -110,9 +127,14 @@ class ScaledGemm:
 
     def run(self, A, a_scale, B, b_scale, D, C=None, bias=None, row_scale=None, offsets=None, alpha=1.0,
             beta=0.0, workspace=None, stream=None):
-        a = gemm_scaled_args(_addr(A), _addr(a_scale), _addr(B), _addr(b_scale), _addr(C), _addr(D),
-                             _addr(bias), _addr(row_scale), _addr(offsets), alpha, beta, _addr(workspace))
-        _check(lib().gemm_scaled_run(self.handle, ctypes.byref(a), _stream(stream)), "gemm_scaled_run")
+        a = gemm_scaled_args(_addr(A), _addr(a_scale), _addr(B), _addr(b_scale), None if C is None else _addr(C),
+                             _addr(D), None if bias is None else _addr(bias),
+                             None if row_scale is None else _addr(row_scale),
+                             None if offsets is None else _addr(offsets), alpha, beta,
+                             None if workspace is None else _addr(workspace))
+        rc = _lib.gemm_scaled_run(self.handle, ctypes.byref(a), _stream(stream))
+        if rc:
+            raise GemmError(rc, "gemm_scaled_run")
 
     def close(self):
         if self.handle:
@@ -126,25 +148,35 @@ class ScaledGemm:
             pass
 
 
-_TYPE_CODES = None
+_TYPE_CODES = {}
 
 
 def type_code(t) -> int:
-    """gemm_dtype of a float32, float16 or bfloat16 tensor."""
-    global _TYPE_CODES
-    if _TYPE_CODES is None:
+    """gemm_dtype of a float32, float16 or bfloat16 tensor, -1 of any other."""
+    if not _TYPE_CODES:
         import torch
-        _TYPE_CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+        _TYPE_CODES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
     return _TYPE_CODES.get(t.dtype, -1)
 
 
-def _codes(t, what):
-    """(address, row stride) of a two-dimensional tensor of bytes with contiguous rows."""
-    if t is None:
-        return None, 0
-    if t.dim() != 2 or t.element_size() != 1 or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise GemmError(GEMM_ERR_INVALID_ARG, what)
-    return t.data_ptr(), max(t.stride(0), t.shape[1])
+def _codes(t, rows, cols):
+    """(address, row stride) of a rows x cols tensor of bytes with contiguous rows; None: another."""
+    if t.shape != (rows, cols) or t.element_size() != 1:
+        return None
+    step, one = t.stride()
+    if one != 1 and cols > 1:
+        return None
+    return t.data_ptr(), step if step > cols else cols
+
+
+def _scale(t, rows, cols):
+    """(address, strides) of a rows x cols float32 tensor; None: another."""
+    if t.shape != (rows, cols) or _TYPE_CODES.get(t.dtype, -1) != 0:
+        return None
+    return (t.data_ptr(), *t.stride())
+
+
+_NO_CODES, _NO_SCALE = (None, 0), (None, 0, 0)
 
 
 def quantize(x, q=None, scale=None, qt=None, scale_t=None, block_rows=1, pow2=False, row_index=None,
@@ -155,30 +187,25 @@ def quantize(x, q=None, scale=None, qt=None, scale_t=None, block_rows=1, pow2=Fa
     qt up to a multiple of 16 are the caller's too (behind the last row as well) and are set to
     zero, so that a product may count them in K.  Shapes that do not fit each other raise
     GemmError."""
-    import torch
-    what = "quantize"
-    if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
-        raise GemmError(GEMM_ERR_INVALID_ARG, what)
-    cols, rows = x.shape[1], x.shape[0] if row_index is None else row_index.numel()
-    rb, cb = -(-rows // 128), -(-cols // 128)
-    for t, shape in ((q, (rows, cols)), (qt, (cols, rows)),
-                     (scale, (rows if block_rows == 1 else rb, cb)), (scale_t, (cols, rb))):
-        if t is not None and tuple(t.shape) != shape:
-            raise GemmError(GEMM_ERR_INVALID_ARG, what)
-    for t in (scale, scale_t):
-        if t is not None and t.dtype != torch.float32:
-            raise GemmError(GEMM_ERR_INVALID_ARG, what)
-    if row_index is not None and (row_index.dtype != torch.int32 or not row_index.is_contiguous()):
-        raise GemmError(GEMM_ERR_INVALID_ARG, what)
-    a = quant_args()
-    a.x, a.x_type, a.block_rows, a.pow2, a.index_div = x.data_ptr(), type_code(x), block_rows, int(pow2), index_div
-    a.rows, a.cols, a.ldx, a.x_rows = rows, cols, max(x.stride(0), cols), x.shape[0]
-    a.row_index = _addr(row_index)
-    a.q, a.ldq = _codes(q, what)
-    a.qt, a.ldqt = _codes(qt, what)
-    if scale is not None:
-        a.scale, a.scale_r, a.scale_c = scale.data_ptr(), scale.stride(0), scale.stride(1)
-    if scale_t is not None:
-        a.scale_t, a.scale_t_c, a.scale_t_r = scale_t.data_ptr(), scale_t.stride(0), scale_t.stride(1)
-    a.pad = int(pad)
-    _check(lib().quant_blocks(ctypes.byref(a), _stream(stream)), "quant_blocks")
+    code = type_code(x)
+    ok = x.dim() == 2
+    if ok:
+        x_rows, cols = x.shape
+        step, one = x.stride()
+        rows, index = x_rows, None
+        if row_index is not None:
+            rows, index = row_index.numel(), row_index.data_ptr()
+            ok = row_index.element_size() == 4 and not row_index.is_floating_point() and row_index.is_contiguous()
+        rb, cb = -(-rows // 128), -(-cols // 128)
+        q_at = _NO_CODES if q is None else _codes(q, rows, cols)
+        qt_at = _NO_CODES if qt is None else _codes(qt, cols, rows)
+        s_at = _NO_SCALE if scale is None else _scale(scale, rows if block_rows == 1 else rb, cb)
+        st_at = _NO_SCALE if scale_t is None else _scale(scale_t, cols, rb)
+        ok = ok and (one == 1 or cols <= 1) and q_at and qt_at and s_at and st_at
+    if not ok:
+        raise GemmError(GEMM_ERR_INVALID_ARG, "quantize")
+    a = quant_args(x.data_ptr(), code, block_rows, pow2, index_div, rows, cols, step if step > cols else cols, index,
+                   x_rows, *q_at, *s_at, *qt_at, *st_at, pad)
+    rc = (_lib or lib()).quant_blocks(ctypes.byref(a), _stream(stream))
+    if rc:
+        raise GemmError(rc, "quant_blocks")
