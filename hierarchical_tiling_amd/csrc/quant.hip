@@ -140,6 +140,62 @@ __global__ __launch_bounds__(256) void quant_rows(const QParams p, int64_t units
   if ((lane & 15) == 0 && c < p.cols) p.scale[r * p.scale_r + c / 128 * p.scale_c] = s.scale;
 }
 
+// 8 x 8 values of a lane.  16-bit types stay packed, two to a register, and their magnitudes are
+// compared as 16-bit integers (they are ordered alike, infinity and NaN on top).
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+template <int XT> struct Patch {
+  u32x4 w[8];
+  __device__ __forceinline__ void load(const QParams& p, int i, int64_t s, int64_t c) {
+    const u16* src = (const u16*)p.x + s * p.ldx + c;
+    w[i] = u32x4{0, 0, 0, 0};
+    if (s >= 0 && p.x_vec && c + 8 <= p.cols) {
+      w[i] = *reinterpret_cast<const u32x4*>(src);
+    } else if (s >= 0) {
+      static_for<8>([&](auto e) { if (c + e < p.cols) w[i][(int)e / 2] |= (u32)src[(int)e] << (16 * (e % 2)); });
+    }
+  }
+  template <int I, int J> __device__ __forceinline__ float at() const {
+    if constexpr (XT == DT_BF16) return __builtin_bit_cast(float, J % 2 ? w[I][J / 2] & 0xffff0000u : w[I][J / 2] << 16);
+    else return f16_to_f32((u16)(w[I][J / 2] >> (16 * (J % 2))));
+  }
+  __device__ __forceinline__ static u32 max2(u32 a, u32 b) {
+    return __builtin_bit_cast(u32, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+  }
+  __device__ __forceinline__ static u32 wide(u32 m) {  // the fp32 bits of a 16-bit magnitude
+    return XT == DT_BF16 ? m << 16 : __builtin_bit_cast(u32, f16_to_f32((u16)m));
+  }
+  // largest magnitude of row i / of each column over the 8 rows, as fp32 bits
+  __device__ __forceinline__ u32 row_top(int i) const {
+    u32 m = 0;
+    static_for<4>([&](auto d) { m = max2(m, w[i][(int)d] & 0x7fff7fffu); });
+    return wide(max(m & 0xffffu, m >> 16));
+  }
+  __device__ __forceinline__ void col_top(u32 (&top)[8]) const {
+    static_for<4>([&](auto d) {
+      u32 m = 0;
+      static_for<8>([&](auto i) { m = max2(m, w[i][(int)d] & 0x7fff7fffu); });
+      top[2 * d] = wide(m & 0xffffu);
+      top[2 * d + 1] = wide(m >> 16);
+    });
+  }
+};
+template <> struct Patch<DT_F32> {
+  float v[8][8];
+  __device__ __forceinline__ void load(const QParams& p, int i, int64_t s, int64_t c) { load8<DT_F32>(p, s, c, v[i]); }
+  template <int I, int J> __device__ __forceinline__ float at() const { return v[I][J]; }
+  __device__ __forceinline__ u32 row_top(int i) const {
+    u32 m = 0;
+    static_for<8>([&](auto j) { m = max(m, mag(v[i][j])); });
+    return m;
+  }
+  __device__ __forceinline__ void col_top(u32 (&top)[8]) const {
+    static_for<8>([&](auto j) {
+      top[j] = 0;
+      static_for<8>([&](auto i) { top[j] = max(top[j], mag(v[i][j])); });
+    });
+  }
+};
+
 // A 128 x 128 tile: row-major and transposed codes from one read, with scales by row and by
 // column, or one scale for the tile.  Thread (ty, lx) holds rows 8 ty .. + 7 of columns 8 lx .. + 7;
 // the transposed codes go through LDS (chunk ^ column / 8, so that the 16 lanes of a write fall on
@@ -152,57 +208,55 @@ __global__ __launch_bounds__(256) void quant_tiles(const QParams p, int tiles_c)
   const int64_t rb = blockIdx.x / tiles_c, cb = blockIdx.x % tiles_c;
   const int64_t r0 = rb * 128 + ty * 8, c0 = cb * 128 + lx * 8;
   if (tid < 128) colmax[tid] = 0;
-  float v[8][8];
+  Patch<XT> v;
   static_for<8>([&](auto i) {
     const int64_t r = r0 + i;
-    load8<XT>(p, r < p.rows ? source_row(p, r) : -1, c0, v[i]);
+    v.load(p, i, r < p.rows ? source_row(p, r) : -1, c0);
   });
   __syncthreads();
-  u32 rm[8];
-  static_for<8>([&](auto i) {
-    rm[i] = 0;
-    static_for<8>([&](auto j) { rm[i] = max(rm[i], mag(v[i][j])); });
-  });
   Scale tile;
   if (p.block) {
     u32 m = 0;
-    static_for<8>([&](auto i) { m = max(m, rm[i]); });
+    static_for<8>([&](auto i) { m = max(m, v.row_top(i)); });
     m = row_max(m);
     if (lx == 0) atomicMax(&colmax[0], m);  // a maximum: the same whatever the order
     __syncthreads();
     tile = scale_of(colmax[0], p.pow2);
     if (tid == 0) p.scale[rb * p.scale_r + cb * p.scale_c] = tile.scale;
   } else if (p.qt) {
+    u32 top[8];
+    v.col_top(top);
     static_for<8>([&](auto j) {
-      u32 m = 0;
-      static_for<8>([&](auto i) { m = max(m, mag(v[i][j])); });
+      u32 m = top[j];
       m = max(m, (u32)__shfl_xor((int)m, 16, 64));
       m = max(m, (u32)__shfl_xor((int)m, 32, 64));
       if ((tid & 48) == 0) atomicMax(&colmax[lx * 8 + j], m);
     });
     __syncthreads();
   }
+  if (p.qt) {
+    static_for<8>([&](auto j) {
+      const int col = lx * 8 + j;
+      const Scale s = p.block ? tile : scale_of(colmax[col], p.pow2);
+      const u32 lo = keep(codes4(v.template at<0, j>(), v.template at<1, j>(), v.template at<2, j>(), v.template at<3, j>(), s), p.rows - r0);
+      const u32 hi = keep(codes4(v.template at<4, j>(), v.template at<5, j>(), v.template at<6, j>(), v.template at<7, j>(), s), p.rows - r0 - 4);
+      turned[col * 16 + (((ty >> 1) ^ (lx & 7)) << 1 | (ty & 1))] = (uint64_t)hi << 32 | lo;
+      if (!p.block && ty == 0 && c0 + j < p.cols)
+        p.scale_t[(c0 + j) * p.scale_t_c + rb * p.scale_t_r] = s.scale;
+    });
+  }
   if (p.q) {
     static_for<8>([&](auto i) {
       const int64_t r = r0 + i;
-      const Scale s = p.block ? tile : scale_of(row_max(rm[i]), p.pow2);
+      const Scale s = p.block ? tile : scale_of(row_max(v.row_top(i)), p.pow2);
       if (r < p.rows) {
-        store8(p, r, c0, keep(codes4(v[i][0], v[i][1], v[i][2], v[i][3], s), p.cols - c0),
-               keep(codes4(v[i][4], v[i][5], v[i][6], v[i][7], s), p.cols - c0 - 4));
+        store8(p, r, c0, keep(codes4(v.template at<i, 0>(), v.template at<i, 1>(), v.template at<i, 2>(), v.template at<i, 3>(), s), p.cols - c0),
+               keep(codes4(v.template at<i, 4>(), v.template at<i, 5>(), v.template at<i, 6>(), v.template at<i, 7>(), s), p.cols - c0 - 4));
         if (!p.block && lx == 0) p.scale[r * p.scale_r + cb * p.scale_c] = s.scale;
       }
     });
   }
   if (!p.qt) return;
-  static_for<8>([&](auto j) {
-    const int col = lx * 8 + j;
-    const Scale s = p.block ? tile : scale_of(colmax[col], p.pow2);
-    const u32 lo = keep(codes4(v[0][j], v[1][j], v[2][j], v[3][j], s), p.rows - r0);
-    const u32 hi = keep(codes4(v[4][j], v[5][j], v[6][j], v[7][j], s), p.rows - r0 - 4);
-    turned[col * 16 + (((ty >> 1) ^ (lx & 7)) << 1 | (ty & 1))] = (uint64_t)hi << 32 | lo;
-    if (!p.block && ty == 0 && c0 + j < p.cols)
-      p.scale_t[(c0 + j) * p.scale_t_c + rb * p.scale_t_r] = s.scale;
-  });
   __syncthreads();
 #pragma unroll
   for (int it = 0; it < 4; ++it) {

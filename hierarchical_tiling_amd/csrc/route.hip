@@ -9,7 +9,7 @@ namespace htk {
 namespace {
 
 constexpr int kRouteWaves = 16, kRouteChunk = 2048, kRouteBlocks = 256;
-constexpr int kLossWaves = 8, kLossBlocks = 256;
+constexpr int kLossWaves = 16, kLossBlocks = 256;
 
 // ---- order ---------------------------------------------------------------------------------
 struct RParams {
@@ -18,6 +18,9 @@ struct RParams {
   int64_t ld_ids, rows;
   int n, topk, experts, align;   // n: assignments
   int chunk;                     // assignments per workgroup
+  int bits;                      // of an expert's number
+  int topk_shift;                // s of expert_of
+  uint64_t topk_inverse;         // ceil(2^s / topk)
   int32_t* counts;
   int32_t* offsets;
   int32_t* order;
@@ -25,19 +28,20 @@ struct RParams {
   int32_t* hist;                 // gridDim.x x experts
 };
 
-// The expert of assignment i, or -1 when it is dropped.
+// The expert of assignment i, or -1 when it is dropped.  The division is one multiplication:
+// floor(i / k) = floor(i * ceil(2^36 / k) / 2^36) for i < 2^30 and k <= 64, since the excess of the
+// rounded factor, below i / 2^36 < 1 / 64, is less than the 1 / k to the next whole number.
 __device__ __forceinline__ int expert_of(const RParams& p, int i) {
-  const int t = i / p.topk;
+  const int t = (int)((uint64_t)i * p.topk_inverse >> p.topk_shift);
   if (p.mask && !p.mask[t]) return -1;
   const int e = p.ids[(int64_t)t * p.ld_ids + (i - t * p.topk)];
   return e >= 0 && e < p.experts ? e : -1;
 }
 
 // Lanes of the wave that hold the same expert (dropped lanes match nothing of interest).
-__device__ __forceinline__ unsigned long long same_expert(int e) {
+__device__ __forceinline__ unsigned long long same_expert(int e, int bits) {
   unsigned long long m = ~0ull;
-#pragma unroll
-  for (int b = 0; b < 10; ++b) {
+  for (int b = 0; b < bits; ++b) {
     const unsigned long long s = __ballot((e >> b) & 1);
     m &= (e >> b) & 1 ? s : ~s;
   }
@@ -88,31 +92,39 @@ __global__ __launch_bounds__(1024) void route_place(const RParams p) {
   __shared__ int sums[kRouteWaves];
   const int E = p.experts, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int b = blockIdx.x, nb = gridDim.x;
-  for (int i = tid; i < kRouteWaves * E; i += 1024) sh[i] = 0;
-  __syncthreads();
   const int64_t begin = (int64_t)b * p.chunk, end = min((int64_t)p.n, begin + p.chunk);
   const int run = (p.chunk + kRouteWaves - 1) / kRouteWaves;
   const int64_t w0 = min(begin + (int64_t)wave * run, end), w1 = min(w0 + run, end);
+  // the experts of the wave's first steps stay in registers from the count to the placing
+  constexpr int KEPT = kRouteChunk / kRouteWaves / 64;
+  int kept[KEPT];
+  static_for<KEPT>([&](auto k) {
+    const int64_t i = w0 + k * 64 + lane;
+    kept[k] = i < w1 ? expert_of(p, (int)i) : -1;
+  });
+  // thread e: its expert's total and the part in earlier chunks (loads that wait for nothing here)
+  int before = 0, count = 0;
+  if (tid < E && nb > 1) {
+#pragma unroll 16
+    for (int c = 0; c < nb; ++c) {
+      const int v = p.hist[(int64_t)c * E + tid];
+      before += c < b ? v : 0;
+      count += v;
+    }
+  }
+  for (int i = tid; i < kRouteWaves * E; i += 1024) sh[i] = 0;
+  __syncthreads();
   int* mine = sh + wave * E;
-  for (int64_t i = w0 + lane; i < w1; i += 64) {
+  static_for<KEPT>([&](auto k) {
+    if (kept[k] >= 0) atomicAdd(&mine[kept[k]], 1);
+  });
+  for (int64_t i = w0 + KEPT * 64 + lane; i < w1; i += 64) {
     const int e = expert_of(p, (int)i);
     if (e >= 0) atomicAdd(&mine[e], 1);
   }
   __syncthreads();
-  // thread e: its expert's total and the part in earlier chunks
-  int before = 0, count = 0;
-  if (tid < E) {
-    if (nb == 1) {
-      for (int w = 0; w < kRouteWaves; ++w) count += sh[w * E + tid];
-    } else {
-#pragma unroll 8
-      for (int c = 0; c < nb; ++c) {
-        const int v = p.hist[(int64_t)c * E + tid];
-        before += c < b ? v : 0;
-        count += v;
-      }
-    }
-  }
+  if (tid < E && nb == 1)
+    for (int w = 0; w < kRouteWaves; ++w) count += sh[w * E + tid];
   const int room = (count + p.align - 1) / p.align * p.align;
   int total;
   const int first = block_scan(tid < E ? room : 0, sums, &total);
@@ -136,10 +148,8 @@ __global__ __launch_bounds__(1024) void route_place(const RParams p) {
     for (int64_t r = total + (int64_t)b * 1024 + tid; r < p.rows; r += (int64_t)nb * 1024) p.order[r] = -1;
   __syncthreads();
   volatile int* next = mine;        // this wave's own; its LDS accesses keep their order
-  for (int64_t s = w0; s < w1; s += 64) {
-    const int i = (int)s + lane;
-    const int e = i < w1 ? expert_of(p, i) : -1;
-    const unsigned long long same = same_expert(e);
+  auto place = [&](int64_t i, int e) {
+    const unsigned long long same = same_expert(e, p.bits);
     const int rank = __popcll(same & ((1ull << lane) - 1));
     int at = -1;
     if (e >= 0) at = next[e] + rank;
@@ -148,8 +158,13 @@ __global__ __launch_bounds__(1024) void route_place(const RParams p) {
     __builtin_amdgcn_wave_barrier();
     if (i < w1) {
       if (p.slot) p.slot[i] = at;
-      if (p.order && at >= 0) p.order[at] = i;
+      if (p.order && at >= 0) p.order[at] = (int)i;
     }
+  };
+  static_for<KEPT>([&](auto k) { if (w0 + k * 64 < w1) place(w0 + k * 64 + lane, kept[k]); });
+  for (int64_t s = w0 + KEPT * 64; s < w1; s += 64) {
+    const int64_t i = s + lane;
+    place(i, i < w1 ? expert_of(p, (int)i) : -1);
   }
 }
 
@@ -188,83 +203,121 @@ template <> struct Elem<DT_BF16> {
   __device__ static u16 down(float v) { return f32_to_bf16(v); }
 };
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-  return v;
+// Sum / maximum over the lanes of a wave, the same in all: DPP steps within rows of 16 and across
+// them leave it in the last lane.
+template <bool MAX> __device__ __forceinline__ float wave_all(float v) {
+  constexpr int idle = MAX ? (int)0xff800000 : 0;   // -infinity or 0 from lanes that do not exist
+  auto step = [&](auto ctrl, auto rows) {
+    const float o = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+        idle, __builtin_bit_cast(int, v), decltype(ctrl)::value, decltype(rows)::value, 0xf, false));
+    v = MAX ? fmaxf(v, o) : v + o;
+  };
+  step(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xf>{});  // row_shr:1
+  step(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xf>{});
+  step(std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xf>{});
+  step(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xf>{});
+  step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});  // row_bcast:15
+  step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});  // row_bcast:31
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
-// Softmax of one row, lane l holding experts l, l + 64, ...; zero in all for a row of -infinity.
-// The maximum keeps a NaN out, the sum carries it to every probability.
-template <int T, int NE>
-__device__ __forceinline__ void softmax_row(const BParams& p, int64_t t, int lane, float (&v)[NE]) {
-  const typename Elem<T>::S* x = (const typename Elem<T>::S*)p.logits + t * p.ld;
-  float top = -__builtin_inff();
-  static_for<NE>([&](auto i) {
-    const int e = lane + 64 * i;
-    v[i] = e < p.experts ? Elem<T>::up(x[e]) : -__builtin_inff();
-    top = fmaxf(top, v[i]);
+// Rows a wave has in hand at once, so that their loads and reductions overlap.
+template <int NE> constexpr int rows_at_once() { return NE >= 16 ? 2 : 4; }
+
+// Softmax of R rows t, t + step, ... below `end`, lane l holding experts l, l + 64, ...; zero in all
+// for a row of -infinity and for rows that are masked or past the end.  The
+// maximum keeps a NaN out, the sum carries it to every probability.  Returns the rows that count,
+// a bit each.
+template <int T, int NE, int R>
+__device__ __forceinline__ int softmax_rows(const BParams& p, int64_t t, int64_t step, int64_t end, int lane,
+                                            float (&v)[R][NE]) {
+  bool live[R];
+  static_for<R>([&](auto q) {
+    const int64_t r = t + q * step;
+    live[q] = r < end && (!p.mask || p.mask[r]);
   });
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-  const float base = top == -__builtin_inff() ? 0.f : top;
-  float sum = 0.f;
-  static_for<NE>([&](auto i) {
-    v[i] = expf(v[i] - base);
-    sum += v[i];
+  static_for<R>([&](auto q) {
+    const typename Elem<T>::S* x = (const typename Elem<T>::S*)p.logits + (t + q * step) * p.ld;
+    static_for<NE>([&](auto i) {
+      const int e = lane + 64 * i;
+      v[q][i] = t + q * step < end && e < p.experts ? Elem<T>::up(x[e]) : -__builtin_inff();
+    });
   });
-  sum = wave_sum(sum);
-  const float r = sum == 0.f ? 0.f : 1.f / sum;
-  static_for<NE>([&](auto i) { v[i] *= r; });
+  // (a masked row's values are loaded beside its mask, not behind it, and dropped)
+  static_for<R>([&](auto q) { static_for<NE>([&](auto i) { v[q][i] = live[q] ? v[q][i] : -__builtin_inff(); }); });
+  int bits = 0;
+  static_for<R>([&](auto q) {
+    float top = -__builtin_inff();
+    static_for<NE>([&](auto i) { top = fmaxf(top, v[q][i]); });
+    top = wave_all<true>(top);
+    const float base = top == -__builtin_inff() ? 0.f : top;
+    float sum = 0.f;
+    static_for<NE>([&](auto i) {
+      v[q][i] = expf(v[q][i] - base);
+      sum += v[q][i];
+    });
+    sum = wave_all<false>(sum);
+    const float r = sum == 0.f ? 0.f : 1.f / sum;
+    static_for<NE>([&](auto i) { v[q][i] *= r; });
+    bits |= live[q] ? 1 << q : 0;
+  });
+  return bits;
 }
 
-// prob and loss from the workgroups' sums, added in order, in double.
+// prob and loss from the workgroups' sums, added in a fixed order, in double: thread (g, quad) takes
+// four experts of every G-th workgroup, then the G sums of an expert are added.
+template <int NT>
 __device__ __forceinline__ void finish_loss(const BParams& p, int blocks) {
-  __shared__ double part[1024];
+  __shared__ double part[NT * 4];
   __shared__ int n_live;
-  const int tid = threadIdx.x, nt = blockDim.x;
+  const int tid = threadIdx.x, E = p.experts, quads = (E + 3) / 4, G = NT / quads;
   if (tid == 0) n_live = 0;
   __syncthreads();
   int n = 0;
-  for (int b = tid; b < blocks; b += nt) n += p.partial_n[b];
+  for (int b = tid; b < blocks; b += NT) n += p.partial_n[b];
+  const int my_count = tid < E ? p.counts[tid] : 0;   // beside the sums' loads, not behind them
+  const int g = tid / quads, e0 = (tid - g * quads) * 4;
+  if (g < G) {
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    if (E % 4 == 0) {
+#pragma unroll 16
+      for (int b = g; b < blocks; b += G) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(p.partial + (int64_t)b * E + e0);
+        static_for<4>([&](auto i) { s[i] += v[(int)i]; });
+      }
+    } else {
+#pragma unroll 4
+      for (int b = g; b < blocks; b += G)
+        static_for<4>([&](auto i) { s[i] += e0 + i < E ? p.partial[(int64_t)b * E + e0 + i] : 0.f; });
+    }
+    static_for<4>([&](auto i) { part[g * quads * 4 + e0 + i] = s[i]; });
+  }
   if (n) atomicAdd(&n_live, n);     // integers: any order gives the same sum
   __syncthreads();
   n = n_live;
-  // G threads for each expert, each over every G-th block; their sums are then added in order
-  int G = 1;
-  while (2 * G * p.experts <= nt && 2 * G <= blocks) G *= 2;
   double dot = 0.0;
-  for (int e0 = 0; e0 < p.experts; e0 += nt / G) {
-    const int wide = min(p.experts - e0, nt / G), e = e0 + tid % wide, q = tid / wide;
+  static_assert(NT >= ROUTE_MAX_EXPERTS, "a thread for each expert");
+  if (tid < E) {
     double s = 0.0;
-    if (q < G) {
-#pragma unroll 4
-      for (int b = q; b < blocks; b += G) s += p.partial[(int64_t)b * p.experts + e];
-      part[q * wide + tid % wide] = s;
-    }
-    __syncthreads();
-    if (tid < wide) {
-      s = 0.0;
-      for (int g = 0; g < G; ++g) s += part[g * wide + tid];
-      const double mean = n > 0 ? s / n : 0.0;
-      p.prob[e0 + tid] = (float)mean;
-      dot += mean * p.counts[e0 + tid];
-    }
-    __syncthreads();
+    for (int q = 0; q < G && q < blocks; ++q) s += part[q * quads * 4 + tid];
+    const double mean = n > 0 ? s / n : 0.0;
+    p.prob[tid] = (float)mean;
+    dot = mean * my_count;
   }
+  __syncthreads();
   part[tid] = dot;
   __syncthreads();
-  for (int d = 512; d > 0; d >>= 1) {
-    if (tid < d && tid + d < nt) part[tid] += part[tid + d];
-    __syncthreads();
+  if (tid < 64) {
+    for (int w = 1; w < NT / 64; ++w) dot += part[w * 64 + tid];
+    for (int d = 32; d > 0; d >>= 1) dot += __shfl_xor(dot, d, 64);
   }
   if (tid == 0) {
-    *p.loss = n > 0 ? (float)(p.coef * part[0] * p.experts / ((double)p.topk * n)) : 0.f;
+    *p.loss = n > 0 ? (float)(p.coef * dot * E / ((double)p.topk * n)) : 0.f;
     *p.live = n;
   }
 }
 
-// Sums of the probabilities over each workgroup's tokens: a wave takes every 8th of them.
+// Sums of the probabilities over each workgroup's tokens: a wave takes every 16th of them.
 template <int T, int NE>
 __global__ __launch_bounds__(kLossWaves * 64) void balance_sums(const BParams p) {
   extern __shared__ float sums[];   // [waves][experts]
@@ -274,12 +327,11 @@ __global__ __launch_bounds__(kLossWaves * 64) void balance_sums(const BParams p)
   float acc[NE];
   static_for<NE>([&](auto i) { acc[i] = 0.f; });
   int n = 0;
-  for (int64_t t = t0 + wave; t < t1; t += kLossWaves) {
-    if (p.mask && !p.mask[t]) continue;
-    float v[NE];
-    softmax_row<T, NE>(p, t, lane, v);
-    static_for<NE>([&](auto i) { acc[i] += v[i]; });
-    ++n;
+  constexpr int R = rows_at_once<NE>();
+  for (int64_t t = t0 + wave; t < t1; t += R * kLossWaves) {
+    float v[R][NE];
+    n += __popc(softmax_rows<T, NE, R>(p, t, kLossWaves, t1, lane, v));
+    static_for<R>([&](auto q) { static_for<NE>([&](auto i) { acc[i] += v[q][i]; }); });
   }
   static_for<NE>([&](auto i) {
     if (lane + 64 * i < p.experts) sums[wave * p.experts + lane + 64 * i] = acc[i];
@@ -299,11 +351,11 @@ __global__ __launch_bounds__(kLossWaves * 64) void balance_sums(const BParams p)
   if (gridDim.x == 1) {             // one workgroup has all the sums: finish here
     __threadfence_block();
     __syncthreads();
-    finish_loss(p, 1);
+    finish_loss<kLossWaves * 64>(p, 1);
   }
 }
 
-__global__ __launch_bounds__(1024) void balance_finish(const BParams p, int blocks) { finish_loss(p, blocks); }
+__global__ __launch_bounds__(1024) void balance_finish(const BParams p, int blocks) { finish_loss<1024>(p, blocks); }
 
 // g is taken relative to an even load, (experts * counts - topk * n) as an integer: the constant
 // drops out of g - sum p g, and what is left has no cancellation to lose bits to.
@@ -319,20 +371,21 @@ __global__ __launch_bounds__(256) void balance_slopes(const BParams p) {
     const int e = lane + 64 * i;
     g[i] = e < p.experts ? scale * (float)((int64_t)p.counts[e] * p.experts - (int64_t)p.topk * n) : 0.f;
   });
-  for (int64_t t = w; t < p.tokens; t += waves) {
-    float v[NE];
-    if (n == 0 || (p.mask && !p.mask[t])) {
-      static_for<NE>([&](auto i) { v[i] = 0.f; });
-    } else {
-      softmax_row<T, NE>(p, t, lane, v);
+  constexpr int R = rows_at_once<NE>();
+  for (int64_t t = w; t < p.tokens; t += R * waves) {
+    float v[R][NE];
+    const int live = softmax_rows<T, NE, R>(p, t, waves, p.tokens, lane, v);
+    static_for<R>([&](auto q) {
       float s = 0.f;
-      static_for<NE>([&](auto i) { s += v[i] * g[i]; });
-      s = wave_sum(s);
-      static_for<NE>([&](auto i) { v[i] *= g[i] - s; });
-    }
-    typename Elem<T>::S* d = (typename Elem<T>::S*)p.d_logits + t * p.ld_d;
-    static_for<NE>([&](auto i) {
-      if (lane + 64 * i < p.experts) d[lane + 64 * i] = Elem<T>::down(v[i]);
+      static_for<NE>([&](auto i) { s += v[q][i] * g[i]; });
+      s = wave_all<false>(s);
+      const int64_t r = t + q * waves;
+      if (r < p.tokens) {
+        typename Elem<T>::S* d = (typename Elem<T>::S*)p.d_logits + r * p.ld_d;
+        static_for<NE>([&](auto i) {
+          if (lane + 64 * i < p.experts) d[lane + 64 * i] = Elem<T>::down(live >> q & 1 ? v[q][i] * (g[i] - s) : 0.f);
+        });
+      }
     });
   }
 }
@@ -417,6 +470,11 @@ int route_experts(const route_args* a, void* stream) {
   p.topk = a->topk;
   p.experts = a->experts;
   p.align = a->align;
+  p.bits = 0;
+  while ((1 << p.bits) < a->experts) ++p.bits;
+  p.topk_shift = 30;
+  while ((1 << (p.topk_shift - 30)) < a->topk) ++p.topk_shift;
+  p.topk_inverse = ((uint64_t(1) << p.topk_shift) + a->topk - 1) / a->topk;
   const int64_t blocks = route_blocks(n);
   p.chunk = (int)std::max<int64_t>((n + blocks - 1) / blocks, 1);
   p.counts = a->counts;
@@ -497,7 +555,7 @@ int balance_grad(const balance_grad_args* a, void* stream) {
   p.live = const_cast<int32_t*>(a->live);
   p.d_loss = a->d_loss;
   p.d_logits = a->d_logits;
-  const unsigned blocks = (unsigned)std::min<int64_t>((a->tokens + 3) / 4, 2048);
+  const unsigned blocks = (unsigned)std::min<int64_t>((a->tokens + 3) / 4, 1024);
   hipStream_t s = (hipStream_t)stream;
   with_type(a->type, [&](auto T) {
     with_lanes(a->experts, [&](auto NE) {
