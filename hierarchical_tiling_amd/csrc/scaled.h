@@ -392,8 +392,10 @@ __device__ __forceinline__ void store_outputs(const SParams& p, const STile& s, 
                                               RowOf row_of, int64_t col0, u32x4* lds, int wave) {
   typedef Cols<OT> CM;
   const int lane = threadIdx.x & 63, x = lane & 15, c4 = lane >> 4;
+  __syncthreads();              // the operands in LDS have been read
+  if (col0 >= p.N) return;
   const bool c_ok = !s.C || (p.ldc % CM::VO == 0 && (reinterpret_cast<uintptr_t>(s.C) & 15) == 0);
-  if (s.n0 + BN <= p.N && c_ok && p.split_k <= 1 && p.ldd % CM::VO == 0 &&
+  if (col0 + 16 * RN <= p.N && c_ok && p.split_k <= 1 && p.ldd % CM::VO == 0 &&
       ((reinterpret_cast<uintptr_t>(s.D) | reinterpret_cast<uintptr_t>(p.bias)) & 15) == 0) {
     auto whole = [&](auto act) {
       if (s.C) store_whole<OT, RM, RN, decltype(act)::value, true>(p, s, acc, row_of, col0, x, c4);
@@ -405,23 +407,42 @@ __device__ __forceinline__ void store_outputs(const SParams& p, const STile& s, 
     else whole(std::integral_constant<int, 1>{});
     return;
   }
-  // everything else element by element, a row block of the wave at a time through LDS, so that
-  // the code is a short loop and a row's neighbours are stored together
-  constexpr int W = 16 * RN, PITCH = W + 4;
+  // everything else element by element, a row block of the wave at a time through LDS, so that a
+  // row's neighbours are stored together; a lane has one column, and U rows in hand at once (D may
+  // be C: their C is loaded before any is stored)
+  constexpr int W = 16 * RN, PITCH = W + 4, U = 8;
   static_assert(W == 64, "a lane for each column");
   float* mine = reinterpret_cast<float*>(lds) + wave * 16 * PITCH;
-  __syncthreads();              // the operands in LDS have been read
   const int64_t col = col0 + lane;
+  const bool in = col < p.N;
+  const float bias = p.bias && in ? SOut<OT>::load(p.bias, col) : 0.f;
+  float* plane = p.split_k > 1 ? p.workspace + (int64_t)blockIdx.y * p.M * p.N : nullptr;
   static_for<RM>([&](auto i) {
     static_for<RN>([&](auto j) { *reinterpret_cast<f32x4*>(&mine[x * PITCH + CM::of(j, c4)]) = acc[i][j]; });
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll 1
-    for (int r = 0; r < 16; ++r) {
-      const int64_t row = row_of(i, r);
-      if (row >= s.M || col >= p.N) continue;
-      const float v = mine[r * PITCH + lane];
-      if (p.split_k > 1) p.workspace[((int64_t)blockIdx.y * p.M + row) * p.N + col] = v;
-      else finish_one<OT>(p, s, row, col, v);
+    for (int r0 = 0; r0 < 16; r0 += U) {
+      float v[U], c[U];
+      static_for<U>([&](auto u) {
+        const int64_t row = row_of(i, r0 + u);
+        const bool ok = in && row < s.M;
+        v[u] = mine[(r0 + u) * PITCH + lane];
+        c[u] = 0.f;
+        if (plane) {
+          if (ok) plane[row * p.N + col] = v[u];
+        } else {
+          v[u] *= p.alpha;
+          if (s.row_scale && ok) v[u] *= s.row_scale[row];
+          if (s.C && ok) c[u] = SOut<OT>::load(s.C, row * p.ldc + col);
+        }
+      });
+      if (!plane) {
+        static_for<U>([&](auto u) {
+          const int64_t row = row_of(i, r0 + u);
+          const float y = activate(p.act, (s.C ? v[u] + p.beta * c[u] : v[u]) + bias);
+          if (in && row < s.M) ((OT*)s.D)[row * p.ldd + col] = SOut<OT>::bits(y);
+        });
+      }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   });
@@ -439,7 +460,7 @@ typedef __attribute__((address_space(1))) const void gbl_void_t;
 // lane's A scales are then contiguous in LDS, and its outputs in D.  The placement costs nothing: every DMA lane has its
 // own source address.
 // ------------------------------------------------------------------------------------------
-template <int BM, int BN, int WM, int WN, int ST, int BB, class OT, int OCC, bool PIPE>
+template <int BM, int BN, int WM, int WN, int ST, int BB, class OT, int OCC>
 __global__ __launch_bounds__(WM * WN * 64, OCC) void scaled_tile(const SParams p) {
   constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, RM = TM / 16, RN = TN / 16;
   constexpr int OPS_T = (BM + BN) / 8 / NW;          // tile DMA instructions per wave and block
@@ -521,84 +542,49 @@ __global__ __launch_bounds__(WM * WN * 64, OCC) void scaled_tile(const SParams p
   int slot[2];
   static_for<2>([&](auto u) { slot[u] = swizzled_slot<8>(x, g + 4 * u); });
 
-  // what a wave reads of a block: fragments and scales (a 128-wide B scale is in the A scales)
-  struct Held {
-    Frag<OT> fa[PIPE ? RM : 1], fb[RN];
-    float sa[RM];
-    f32x4 sb[BB == 1 ? RN : 1];
-  };
-  auto read_a = [&](int stage, Frag<OT>& f, int i) {
-    const u32x4* la = lds + stage * STAGE + wm * TM * 8;
-    static_for<2>([&](auto u) { f.set(u, la[i * 128 + slot[u]]); });
-  };
-  auto read = [&](int stage, Held& h) {
+  auto compute = [&](int stage) {
     const u32x4* st = lds + stage * STAGE;
+    const u32x4* la = st + wm * TM * 8;
     const u32x4* lb = st + (BM + wn * TN) * 8;
     const float* ls = reinterpret_cast<const float*>(st + (BM + BN) * 8);
-    static_for<RN>([&](auto j) { static_for<2>([&](auto u) { h.fb[j].set(u, lb[j * 128 + slot[u]]); }); });
-    if constexpr (PIPE) static_for<RM>([&](auto i) { read_a(stage, h.fa[i], i); });
-    static_for<RM>([&](auto i) { h.sa[i] = ls[wm * TM + x * RM + i]; });
+    Frag<OT> fb[RN];
+    static_for<RN>([&](auto j) { static_for<2>([&](auto u) { fb[j].set(u, lb[j * 128 + slot[u]]); }); });
+    float sa[RM];
+    static_for<RM>([&](auto i) { sa[i] = ls[wm * TM + x * RM + i]; });
+    f32x4 sb[BB == 1 ? RN : 1];
     if constexpr (BB == 1) {
-      static_for<RN>([&](auto j) { h.sb[j] = *reinterpret_cast<const f32x4*>(&ls[BM + wn * TN + Cols<OT>::of(j, g)]); });
+      static_for<RN>([&](auto j) { sb[j] = *reinterpret_cast<const f32x4*>(&ls[BM + wn * TN + Cols<OT>::of(j, g)]); });
     } else {
       const float one = ls[BM + wn * TN];
-      static_for<RM>([&](auto i) { h.sa[i] *= one; });
+      static_for<RM>([&](auto i) { sa[i] *= one; });
     }
-  };
-  auto compute = [&](int stage, Held& h) {
     static_for<RM>([&](auto i) {
-      if constexpr (!PIPE) read_a(stage, h.fa[0], i);
+      Frag<OT> fa;
+      static_for<2>([&](auto u) { fa.set(u, la[i * 128 + slot[u]]); });
       f32x4 t[RN];
-      static_for<RN>([&](auto j) { t[j] = mfma_block(h.fb[j], h.fa[PIPE ? (int)i : 0]); });
+      static_for<RN>([&](auto j) { t[j] = mfma_block(fb[j], fa); });
       static_for<RN>([&](auto j) {
         static_for<4>([&](auto r) {
-          const float w = BB == 1 ? h.sa[i] * h.sb[BB == 1 ? (int)j : 0][(int)r] : h.sa[i];
+          const float w = BB == 1 ? sa[i] * sb[BB == 1 ? (int)j : 0][(int)r] : sa[i];
           acc[i][j][(int)r] = __builtin_fmaf(t[j][(int)r], w, acc[i][j][(int)r]);
         });
       });
     });
   };
-  // Block t + 1 has landed for this wave and, behind the barrier, for all; and all are done with
-  // the stage that is refilled next.
-  auto turn = [&]() {
-    wait_counts<(ST - 2) * OPS, true>();
-    barrier_nofence();
-  };
+
   if (nk > 0) {
-    if constexpr (PIPE) {
-      // A block's fragments are read into registers one block ahead of its matrix instructions, so
-      // that no LDS round trip stands in front of them; its stage is then free.
-      static_for<ST>([&](auto q) { dma(q, q); });
-      wait_counts<(ST - 1) * OPS, true>();
+    static_for<ST - 1>([&](auto q) { dma(q, q); });
+    int stage = 0;
+    for (int t = 0; t < nk; ++t) {
+      // block t has landed for this wave and, behind the barrier, for all; the stage refilled
+      // next was last read before it
+      wait_counts<(ST - 2) * OPS, true>();
       barrier_nofence();
-      Held h[2];
-      read(0, h[0]);
-      int stage = 0;               // of block t
-      auto step = [&](int t, Held& now, Held& next) {
-        turn();
-        dma(t + ST, stage);
-        if (++stage == ST) stage = 0;
-        if (t + 1 < nk) read(stage, next);
-        compute(0, now);
-      };
-      for (int t = 0; t < nk; t += 2) {
-        step(t, h[0], h[1]);
-        if (t + 1 >= nk) break;
-        step(t + 1, h[1], h[0]);
-      }
-    } else {
-      static_for<ST - 1>([&](auto q) { dma(q, q); });
-      int stage = 0;
-      for (int t = 0; t < nk; ++t) {
-        turn();
-        int next = stage + ST - 1;
-        if (next >= ST) next -= ST;
-        dma(t + ST - 1, next);
-        Held h;
-        read(stage, h);
-        compute(stage, h);
-        if (++stage == ST) stage = 0;
-      }
+      int next = stage + ST - 1;
+      if (next >= ST) next -= ST;
+      dma(t + ST - 1, next);
+      compute(stage);
+      if (++stage == ST) stage = 0;
     }
     wait_counts<0, true>();  // zero blocks issued past the end
   }
@@ -802,6 +788,7 @@ __global__ __launch_bounds__(512, 1) void scaled_pp(const SParams p) {
                                                in_k ? o + (uint32_t)(cols * p.ldb) : kOobOffset, (int)k, 0, 0);
     });
   };
+  const bool idle = s.M - s.m0 <= g * 128;  // a group without rows keeps the phases, not the work
   constexpr int HELD = 2;           // A fragments read in the read phase
   constexpr int LAG = 2;            // instructions between a sum and its addition
   Frag<u16> fa[RM], fb[RN];
@@ -842,6 +829,7 @@ __global__ __launch_bounds__(512, 1) void scaled_pp(const SParams p) {
       phase_end();
       // compute phase: the sums of an instruction are added LAG instructions later, when they are
       // there; the wave is preferred to the one that reads
+      if (!idle) {
       __builtin_amdgcn_s_setprio(1);
       f32x4 t[LAG + 1];
       float w[RM];
@@ -865,6 +853,7 @@ __global__ __launch_bounds__(512, 1) void scaled_pp(const SParams p) {
         if constexpr (n >= LAG) __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
       });
       __builtin_amdgcn_s_setprio(0);
+      }
       wait_counts<4, true>();
       phase_end();
     }

@@ -1,5 +1,7 @@
 // scaled.hip -- block-scaled e4m3 products: host side of htscaled.h's gemm_scaled_* and the
 // instantiations of the kernels in scaled.h.
+#include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <new>
 
@@ -15,17 +17,24 @@ constexpr int64_t kCUs = 256;
 
 typedef hipError_t (*scaled_launch)(const SParams&, dim3, hipStream_t);
 
-// One kernel: its tile, and its launch for b_block 128 / 1 and bf16 / f32 outputs.
+// One kernel: its tile, its launch for b_block 128 / 1 and bf16 / f32 outputs, and what choose()
+// goes by: workgroups a CU holds at once (occ), waves that share k (kw), microseconds for a block
+// of k while a CU has one workgroup (c1) and while it has occ of them (c2), for bf16 and f32
+// outputs, and for each round of workgroups beside them (round).  Measured on MI355X.
+struct Cost {
+  int occ, kw;
+  float c1[2], c2[2], round;
+};
 struct Variant {
   const char* name;
-  int bm, bn, waves, lds, stream;
+  int bm, bn, waves, lds;
+  Cost cost;
   scaled_launch launch[2][2];
 };
 
 template <int BM, int BN, int WM, int WN, int ST, int OCC, int BB, class OT>
 hipError_t go_tile(const SParams& p, dim3 grid, hipStream_t s) {
-  constexpr bool pipe = sizeof(OT) == 2;
-  hipLaunchKernelGGL((scaled_tile<BM, BN, WM, WN, ST, BB, OT, OCC, pipe>), grid, dim3(WM * WN * 64), 0, s, p);
+  hipLaunchKernelGGL((scaled_tile<BM, BN, WM, WN, ST, BB, OT, OCC>), grid, dim3(WM * WN * 64), 0, s, p);
   return hipGetLastError();
 }
 template <int RM, int NBW, int WK, int R, int OCC, int BB, class OT>
@@ -43,26 +52,28 @@ hipError_t go_pp(const SParams& p, dim3 grid, hipStream_t s) {
   return hipGetLastError();
 }
 
-#define HT_TILE(NAME, BM, BN, WM, WN, ST, OCC)                                                    \
-  {NAME, BM, BN, WM * WN, ST * (BM + BN) * 132, 0,                                                \
+#define HT_TILE(NAME, BM, BN, WM, WN, ST, OCC, ...)                                                    \
+  {NAME, BM, BN, WM * WN, ST * (BM + BN) * 132, __VA_ARGS__,                                             \
    {{&go_tile<BM, BN, WM, WN, ST, OCC, 128, u16>, &go_tile<BM, BN, WM, WN, ST, OCC, 128, float>}, \
     {&go_tile<BM, BN, WM, WN, ST, OCC, 1, u16>, &go_tile<BM, BN, WM, WN, ST, OCC, 1, float>}}}
-#define HT_STREAM(NAME, RM, NBW, WK, R, OCC)                                                      \
-  {NAME, 16 * RM, 16 * NBW, WK, WK * R * (16 * (RM + NBW) * 128 + (16 * (RM + NBW) + 63) / 64 * 256), 1, \
+#define HT_STREAM(NAME, RM, NBW, WK, R, OCC, ...)                                                      \
+  {NAME, 16 * RM, 16 * NBW, WK, WK * R * (16 * (RM + NBW) * 128 + (16 * (RM + NBW) + 63) / 64 * 256), __VA_ARGS__, \
    {{&go_stream<RM, NBW, WK, R, OCC, 128, u16>, &go_stream<RM, NBW, WK, R, OCC, 128, float>},     \
     {&go_stream<RM, NBW, WK, R, OCC, 1, u16>, &go_stream<RM, NBW, WK, R, OCC, 1, float>}}}
 
 enum { V_NARROW, V_S16, V_S16N, V_S32, V_S64, V_T64, V_T128, V_PP, V_COUNT };
+#define HT_COST(...) {__VA_ARGS__}
 const Variant kVariants[V_COUNT] = {
-    {"narrow_64x64", 64, 64, 4, 16384, 0,
+    {"narrow_64x64", 64, 64, 4, 16384, {2, 1, {3.f, 3.f}, {6.f, 6.f}, 2.f},
      {{&go_narrow<128, u16>, &go_narrow<128, float>}, {&go_narrow<1, u16>, &go_narrow<1, float>}}},
-    HT_STREAM("stream_16x32_w4", 1, 2, 4, 3, 2),
-    HT_STREAM("stream_16x16_w8", 1, 1, 8, 4, 1),
-    HT_STREAM("stream_32x32_w4", 2, 2, 4, 3, 1),
-    HT_STREAM("stream_64x32_w4", 4, 2, 4, 3, 1),
-    HT_TILE("tile_64x128_w2x2", 64, 128, 2, 2, 3, 2),
-    HT_TILE("tile_128x128_w2x2", 128, 128, 2, 2, 2, 2),
-    {"pingpong_256x256", 256, 256, 8, 160 * 1024, 0, {{&go_pp, nullptr}, {nullptr, nullptr}}},
+    HT_STREAM("stream_16x32_w4", 1, 2, 4, 3, 2, HT_COST(2, 4, {.38f, .42f}, {.80f, .90f}, 1.5f)),
+    HT_STREAM("stream_16x16_w8", 1, 1, 8, 4, 1, HT_COST(1, 8, {.38f, .40f}, {.38f, .40f}, 2.f)),
+    HT_STREAM("stream_32x32_w4", 2, 2, 4, 3, 1, HT_COST(1, 4, {.55f, .65f}, {.55f, .65f}, 3.f)),
+    HT_STREAM("stream_64x32_w4", 4, 2, 4, 3, 1, HT_COST(1, 4, {1.0f, 1.2f}, {1.0f, 1.2f}, 3.f)),
+    HT_TILE("tile_64x128_w2x2", 64, 128, 2, 2, 3, 2, HT_COST(2, 1, {.43f, .80f}, {.72f, 1.30f}, 1.5f)),
+    HT_TILE("tile_128x128_w2x2", 128, 128, 2, 2, 2, 2, HT_COST(2, 1, {.72f, 1.25f}, {1.09f, 2.00f}, 1.5f)),
+    {"pingpong_256x256", 256, 256, 8, 160 * 1024, {1, 1, {1.40f, 0.f}, {1.40f, 0.f}, 6.f},
+     {{&go_pp, nullptr}, {nullptr, nullptr}}},
 };
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -88,35 +99,71 @@ int64_t row_tiles(const gemm_scaled_s& h, int bm) {
   return h.d.form == GEMM_SCALED_ROWS ? std::min(h.d.M, h.d.M / bm + h.batch) : t;
 }
 
-// Which kernel, by the rows an average product or group has.  (Rule re-measured with the kernels;
-// see the figures at choose().)
+// Expected row tiles of a launch, for groups of rows from a routing that spreads M rows over the
+// groups: the groups that get any, and what a group's last tile leaves empty.
+double expected_row_tiles(const gemm_scaled_s& h, int bm) {
+  const double M = double(h.d.M);
+  if (h.d.form != GEMM_SCALED_ROWS) return std::ceil(M / bm);
+  const double hit = std::max(1.0, h.batch * (1.0 - std::exp(-M / h.batch)));
+  return hit * std::max(1.0, M / hit / bm + 0.4);
+}
+
+// Predicted microseconds of a variant with k in `split` slices: rounds of workgroups at the
+// measured cost of a block, against the time that the operands' bytes take at 5.2 TB/s (the less of
+// the two counts a quarter: they overlap, not fully), plus the second kernel of a split.  Over 45
+// measured products and groups the choice by it was the fastest variant or within 12 % of it but
+// for two (17 and 20 %); a rule on rows alone (streaming kernels up to 64 rows, k split until 512
+// workgroups) cost up to 2.3 times the fastest (1000 rows over 32 experts: 141 against 61 us).
+double predict(const gemm_scaled_s& h, const Variant& v, int split) {
+  const gemm_scaled_desc& d = h.d;
+  const Cost& c = v.cost;
+  const int f32 = d.d_type == GEMM_F32;
+  const double many = d.form == GEMM_SCALED_BATCH || d.form == GEMM_SCALED_K ? double(h.batch) : 1.0;
+  const double wgs = expected_row_tiles(h, v.bm) * up(d.N, v.bn) * many * split;
+  const double k = d.form == GEMM_SCALED_K ? double(d.K) / h.batch : double(d.K);
+  const double steps = std::ceil(std::ceil(k / kSB) / split / c.kw);
+  const double whole = std::floor(wgs / (kCUs * c.occ)), load = wgs / kCUs - whole * c.occ;  // last round's
+  double last = 0.0;
+  if (load > 0.0) last = steps * (c.c1[f32] + (c.c2[f32] - c.c1[f32]) * std::max(0.0, load - 1.0)) + c.round;
+  const double work = 2.0 + whole * (steps * c.c2[f32] + c.round) + last;
+  const double hit = d.form == GEMM_SCALED_ROWS ? h.batch * (1.0 - std::exp(-double(d.M) / h.batch)) : many;
+  const double a_many = d.form == GEMM_SCALED_BATCH ? many : 1.0, b_many = d.form == GEMM_SCALED_K ? 1.0 : hit;
+  const double d_many = d.form == GEMM_SCALED_ROWS ? 1.0 : many;
+  const double bytes = a_many * d.M * d.K + b_many * d.N * d.K + d_many * d.M * d.N * (f32 ? 4.0 : 2.0);
+  const double mem = bytes / 5.2e6;
+  double us = std::max(work, mem) + 0.25 * std::min(work, mem);
+  if (split > 1) us += 6.0 + split * double(d.M) * d.N * 8.0 / 4.0e6;
+  return us;
+}
+
+void set_split(gemm_scaled_s* h, int64_t want) {
+  const int64_t blocks = std::max<int64_t>(up(h->d.K, kSB), 1);
+  want = std::max<int64_t>(1, std::min(want, blocks));
+  h->per = up(blocks, want);
+  h->split = (int)up(blocks, h->per);
+}
+
+// The variant (and, for one product, the split of k) with the least predicted time.
 void choose(gemm_scaled_s* h) {
   const gemm_scaled_desc& d = h->d;
-  h->split = 1;
-  h->per = up(d.K, kSB);
-  if (!h->vec) {
-    h->variant = V_NARROW;
-    return;
-  }
-  const int64_t many = d.form == GEMM_SCALED_BATCH || d.form == GEMM_SCALED_K ? h->batch : 1;
-  const double rows = d.form == GEMM_SCALED_ROWS ? double(d.M) / h->batch : double(d.M);
-  if (rows <= 16) h->variant = up(d.N, 32) * row_tiles(*h, 16) * many >= kCUs ? V_S16 : V_S16N;
-  else if (rows <= 32) h->variant = V_S32;
-  else if (rows <= 64) h->variant = V_S64;
-  else if (up(d.N, 256) * row_tiles(*h, 256) * many >= kCUs && rows > 128 && d.d_type == GEMM_BF16 &&
-           d.b_block == kSB && d.a_scale_m == 1)
-    h->variant = V_PP;
-  else if (up(d.N, 128) * row_tiles(*h, 128) * many >= kCUs) h->variant = V_T128;
-  else h->variant = V_T64;
-  const Variant& v = kVariants[h->variant];
-  if (d.form == GEMM_SCALED_SINGLE) {
-    int64_t want = d.split_k;
-    const int64_t blocks = up(d.K, kSB), tiles = up(d.M, v.bm) * up(d.N, v.bn);
-    if (want == 0 && tiles > 0 && !v.stream) want = std::min<int64_t>(2 * kCUs / std::max<int64_t>(tiles, 1), blocks / 4);
-    want = std::max<int64_t>(1, std::min(want, blocks));
-    if (want > 1) {
-      h->per = up(blocks, want);
-      h->split = (int)up(blocks, h->per);
+  h->variant = V_NARROW;
+  set_split(h, 1);
+  if (!h->vec) return;
+  const int bb = d.b_block == 1, f32 = d.d_type == GEMM_F32;
+  double best = 0.0;
+  for (int i = V_NARROW + 1; i < V_COUNT; ++i) {
+    const Variant& v = kVariants[i];
+    if (!v.launch[bb][f32] || (i == V_PP && d.a_scale_m != 1)) continue;
+    for (int s = 1; s <= 16; s *= 2) {
+      const bool forced = d.split_k > 0 || d.form != GEMM_SCALED_SINGLE;
+      if (forced && s > 1) break;
+      if (s > 1 && (s * 4 > up(d.K, kSB))) break;
+      const double us = predict(*h, v, forced && d.split_k > 1 ? d.split_k : s);
+      if (h->variant == V_NARROW || us < best) {
+        best = us;
+        h->variant = i;
+        set_split(h, forced ? std::max(d.split_k, 1) : s);
+      }
     }
   }
 }
