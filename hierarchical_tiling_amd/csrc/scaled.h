@@ -788,7 +788,6 @@ __global__ __launch_bounds__(512, 1) void scaled_pp(const SParams p) {
                                                in_k ? o + (uint32_t)(cols * p.ldb) : kOobOffset, (int)k, 0, 0);
     });
   };
-  const bool idle = s.M - s.m0 <= g * 128;  // a group without rows keeps the phases, not the work
   constexpr int HELD = 2;           // A fragments read in the read phase
   constexpr int LAG = 2;            // instructions between a sum and its addition
   Frag<u16> fa[RM], fb[RN];
@@ -829,7 +828,6 @@ __global__ __launch_bounds__(512, 1) void scaled_pp(const SParams p) {
       phase_end();
       // compute phase: the sums of an instruction are added LAG instructions later, when they are
       // there; the wave is preferred to the one that reads
-      if (!idle) {
       __builtin_amdgcn_s_setprio(1);
       f32x4 t[LAG + 1];
       float w[RM];
@@ -853,7 +851,6 @@ __global__ __launch_bounds__(512, 1) void scaled_pp(const SParams p) {
         if constexpr (n >= LAG) __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
       });
       __builtin_amdgcn_s_setprio(0);
-      }
       wait_counts<4, true>();
       phase_end();
     }

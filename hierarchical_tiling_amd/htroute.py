@@ -1,5 +1,6 @@
 """ctypes binding of include/htroute.h: expert counts, offsets and row order, and the balance loss
-with its gradient, with argument marshalling only.  Every buffer is the caller's torch tensor.
+with its gradient, with argument marshalling only.  Every buffer is the caller's torch tensor, on
+the current device; shapes and types that do not fit raise GemmError.
 """
 from __future__ import annotations
 
@@ -7,7 +8,7 @@ import ctypes
 
 from . import htgemm
 from .htgemm import GEMM_ERR_INVALID_ARG, GemmError, _check
-from .htscaled import _stream, type_code
+from .htscaled import _elsewhere, _here, type_code
 
 _i32, _i64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
 
@@ -114,7 +115,10 @@ def route(ids, counts, offsets, order=None, slot=None, mask=None, align=1, works
     a = route_args(ids.data_ptr(), _mask(mask, tokens, "route"), tokens, step if step > topk else topk, topk, experts,
                    align, counts.data_ptr(), offsets.data_ptr(), None if order is None else order.data_ptr(), rows,
                    None if slot is None else slot.data_ptr(), _room(workspace, tokens, topk, experts, "route"))
-    rc = _lib.route_experts(ctypes.byref(a), _stream(stream))
+    dev, stream = _here(stream)
+    if _elsewhere(dev, ids, counts, offsets, order, slot, mask, workspace):
+        raise _bad("route")
+    rc = _lib.route_experts(ctypes.byref(a), stream)
     if rc:
         raise GemmError(rc, "route_experts")
 
@@ -140,7 +144,10 @@ def balance_loss(logits, counts, topk, loss, prob, live, mask=None, coef=1.0, wo
     a = balance_args(logits.data_ptr(), type_code(logits), experts, topk, coef, tokens, ld,
                      _mask(mask, tokens, "balance_loss"), counts.data_ptr(), loss.data_ptr(), prob.data_ptr(),
                      live.data_ptr(), _room(workspace, tokens, topk, experts, "balance_loss"))
-    rc = _lib.balance_loss(ctypes.byref(a), _stream(stream))
+    dev, stream = _here(stream)
+    if _elsewhere(dev, logits, counts, loss, prob, live, mask, workspace):
+        raise _bad("balance_loss")
+    rc = _lib.balance_loss(ctypes.byref(a), stream)
     if rc:
         raise GemmError(rc, "balance_loss")
 
@@ -157,6 +164,9 @@ def balance_grad(logits, counts, topk, live, d_loss, d_logits, mask=None, coef=1
     a = balance_grad_args(logits.data_ptr(), type_code(logits), experts, topk, coef, tokens, ld,
                           _mask(mask, tokens, "balance_grad"), counts.data_ptr(), live.data_ptr(), d_loss.data_ptr(),
                           d_logits.data_ptr(), step if step > experts else experts)
-    rc = (_lib or lib()).balance_grad(ctypes.byref(a), _stream(stream))
+    dev, stream = _here(stream)
+    if _elsewhere(dev, logits, counts, live, d_loss, d_logits, mask):
+        raise _bad("balance_grad")
+    rc = (_lib or lib()).balance_grad(ctypes.byref(a), stream)
     if rc:
         raise GemmError(rc, "balance_grad")

@@ -48,20 +48,28 @@ EXPORTED = ["gemm_scaled_create", "gemm_scaled_workspace_size", "gemm_scaled_run
 _lib = None
 
 
-def _stream(s):
-    """The hipStream_t of `s`, or of torch's current stream: as htgemm's, by the shorter way to the
+def _here(s):
+    """(current device, hipStream_t of `s` or of torch's current stream): by the shorter way to the
     raw handle, since these calls are made many times a layer."""
-    if s is not None:
-        return _stream_of(s)
     global _raw_stream, _device
     if _raw_stream is None:
         import torch
         torch.cuda.current_stream()      # initialises the runtime if nothing has
         _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-    return _raw_stream(_device())
+    dev = _device()
+    return dev, _raw_stream(dev) if s is None else _stream_of(s)
 
 
 _raw_stream = _device = None
+
+
+def _elsewhere(dev, *tensors):
+    """Whether any of the tensors (None and addresses aside) is not on device `dev`: a kernel there
+    could not reach it."""
+    for t in tensors:
+        if t is not None and t.__class__ is not int and t.get_device() != dev:
+            return True
+    return False
 
 
 def lib():
@@ -132,7 +140,10 @@ class ScaledGemm:
                              None if row_scale is None else _addr(row_scale),
                              None if offsets is None else _addr(offsets), alpha, beta,
                              None if workspace is None else _addr(workspace))
-        rc = _lib.gemm_scaled_run(self.handle, ctypes.byref(a), _stream(stream))
+        dev, stream = _here(stream)
+        if _elsewhere(dev, A, a_scale, B, b_scale, C, D, bias, row_scale, offsets, workspace):
+            raise GemmError(GEMM_ERR_INVALID_ARG, "gemm_scaled_run")
+        rc = _lib.gemm_scaled_run(self.handle, ctypes.byref(a), stream)
         if rc:
             raise GemmError(rc, "gemm_scaled_run")
 
@@ -185,8 +196,8 @@ def quantize(x, q=None, scale=None, qt=None, scale_t=None, block_rows=1, pow2=Fa
     cols / 128), qt (cols, rows) and scale_t (cols, rows / 128), each any float32 strides.  With
     row_index the result has a row for each of its values.  pad: the bytes between the rows of q and
     qt up to a multiple of 16 are the caller's too (behind the last row as well) and are set to
-    zero, so that a product may count them in K.  Shapes that do not fit each other raise
-    GemmError."""
+    zero, so that a product may count them in K.  Shapes that do not fit each other, and tensors on
+    another device than the current one, raise GemmError."""
     code = type_code(x)
     ok = x.dim() == 2
     if ok:
@@ -206,6 +217,9 @@ def quantize(x, q=None, scale=None, qt=None, scale_t=None, block_rows=1, pow2=Fa
         raise GemmError(GEMM_ERR_INVALID_ARG, "quantize")
     a = quant_args(x.data_ptr(), code, block_rows, pow2, index_div, rows, cols, step if step > cols else cols, index,
                    x_rows, *q_at, *s_at, *qt_at, *st_at, pad)
-    rc = (_lib or lib()).quant_blocks(ctypes.byref(a), _stream(stream))
+    dev, stream = _here(stream)
+    if _elsewhere(dev, x, q, scale, qt, scale_t, row_index):
+        raise GemmError(GEMM_ERR_INVALID_ARG, "quantize")
+    rc = (_lib or lib()).quant_blocks(ctypes.byref(a), stream)
     if rc:
         raise GemmError(rc, "quant_blocks")

@@ -124,3 +124,28 @@ def test_gradients(T, E, k, H, F):
             assert ((dw[e].double() - want).abs() <= 2.0 ** -2.9 * size + 1e-6).all()
         else:
             assert (dw[e] == 0).all()
+
+
+def test_on_another_stream():
+    """The layer's first half on a side stream gives what it gives on the default one."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    T, E, k, H, F = 300, 16, 2, 256, 256
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    ids = torch.rand(T, E, generator=g, device="cuda").topk(k, dim=1).indices.to(torch.int32)
+    w, ws_scale = [torch.stack(t) for t in zip(*(quantised(torch.randn(F, H, generator=g, device="cuda"), block_rows=128)
+                                                 for _ in range(E)))]
+
+    def layer():
+        counts, offsets, order = (torch.empty(n, **I32) for n in (E, E + 1, T * k))
+        R.route(ids, counts, offsets, order, workspace=torch.empty(R.workspace_size(T, k, E), dtype=torch.uint8, device="cuda"))
+        a, sa = quantised(x, row_index=order, index_div=k)
+        return grouped(a, sa, w, ws_scale, offsets, T * k, F, H, act="silu")
+
+    want = layer()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = layer()
+    side.synchronize()
+    assert torch.equal(got, want)

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from hierarchical_tiling_amd import htscaled as S
+from hierarchical_tiling_amd.htgemm import GemmError
 from scaled_util import BLOCK, up
 
 pytestmark = pytest.mark.gpu
@@ -195,6 +196,14 @@ def test_empty_and_misaligned_source():
     S.quantize(x, q, s, qt, st)
     w, ws = steps(x.float().cpu().numpy(), 1, BLOCK, False)
     same(q, w), same(s, ws)
+
+
+def test_tensors_elsewhere_are_refused():
+    x = source(4, 256, "bf16", 1)
+    q, _, s, _ = outputs(4, 256)
+    for args in ((x.cpu(), q, s), (x, q.cpu(), s), (x, q, s.cpu())):
+        with pytest.raises(GemmError):
+            S.quantize(*args)
 
 
 def test_captured_and_replayed():

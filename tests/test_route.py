@@ -3,6 +3,7 @@ import pytest
 import torch
 
 from hierarchical_tiling_amd import htroute as R
+from hierarchical_tiling_amd.htgemm import GemmError
 from scaled_util import up
 
 pytestmark = pytest.mark.gpu
@@ -41,7 +42,8 @@ def ids_of(T, k, E, seed, skew=1.0):
 
 
 @pytest.mark.parametrize("T,k,E", [(0, 2, 4), (1, 1, 1), (1, 3, 5), (7, 2, 1024), (37, 6, 64), (100, 1, 3), (1000, 2, 8),
-                                   (1025, 2, 100), (3000, 8, 256), (5000, 4, 1024), (40000, 2, 60)])
+                                   (1025, 2, 100), (3000, 8, 256), (5000, 4, 1024), (40000, 2, 60),
+                                   (270000, 2, 70)])
 @pytest.mark.parametrize("align", [1, 16, 128])
 def test_route(T, k, E, align):
     ids = ids_of(T, k, E, T + E)
@@ -65,6 +67,21 @@ def test_dropped_and_masked(T):
             assert a.tolist() == b
     only = routed(ids.cuda().contiguous(), 9, 1, order=False, slot=False)
     assert (only[2] == -9).all() and (only[3] == -9).all()
+
+
+def test_tensors_elsewhere_are_refused():
+    ids = ids_of(5, 2, 4, 1)
+    good = [torch.empty(n, **I32) for n in (4, 5, 10, 10)]
+    ws = torch.empty(R.workspace_size(5, 2, 4), dtype=torch.uint8, device="cuda")
+    with pytest.raises(GemmError):
+        R.route(ids, *good, workspace=ws)
+    with pytest.raises(GemmError):
+        R.route(ids.cuda(), *good[:3], good[3].cpu(), workspace=ws)
+    one, live = torch.ones(1, device="cuda"), torch.empty(1, **I32)
+    with pytest.raises(GemmError):
+        R.balance_loss(torch.zeros(5, 4), good[0], 2, one, torch.zeros(4, device="cuda"), live, workspace=ws)
+    with pytest.raises(GemmError):
+        R.balance_grad(torch.zeros(5, 4, device="cuda"), good[0], 2, live, one.cpu(), torch.zeros(5, 4, device="cuda"))
 
 
 def test_one_expert_takes_all():

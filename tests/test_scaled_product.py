@@ -304,9 +304,45 @@ def test_refusals_at_run():
     for change, status in (({"workspace": None}, 1), ({"workspace": ws.data_ptr() + 8}, 1), ({"A": None}, 1),
                            ({"b_scale": None}, 1), ({"D": None}, 1), ({"bias": p.bias}, 1), ({"beta": 1.0}, 1),
                            ({"offsets": torch.zeros(2, dtype=torch.int32, device="cuda")}, 1),
-                           ({"row_scale": p.row_scale}, 1), ({"D": d.data_ptr() + 1}, 4), ({"a_scale": p.sa.data_ptr() + 2}, 4)):
+                           ({"row_scale": p.row_scale}, 1), ({"A": p.a_v.cpu()}, 1), ({"D": d.data_ptr() + 1}, 4), ({"a_scale": p.sa.data_ptr() + 2}, 4)):
         with pytest.raises(GemmError) as err:
             h.run(**{**ok, **change})
         assert err.value.status == status, change
     h.close()
     h.close()
+
+
+@pytest.mark.parametrize("rows,E,N,K", [(3000, 6, 640, 512), (700, 300, 96, 256), (2600, 3, 300, 400)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_many_groups_and_large_groups(rows, E, N, K, out):
+    """Groups of more than a tile's rows, and more groups than lanes, against the product of each."""
+    g = gen(rows)
+    p = Problem(rows, N, K, out=out, seed=rows, spread=1.0)
+    to = torch.sort(torch.randint(0, E, (rows,), generator=g, device="cuda")).values
+    counts = torch.bincount(to, minlength=E)
+    offsets = torch.cat([torch.zeros_like(counts[:1]), counts.cumsum(0)]).to(torch.int32)
+    b = torch.stack([codes(g, N, K) for _ in range(E)])
+    kb = up(K, BLOCK)
+    sb = scales(g, E, up(N, BLOCK), kb)
+    h = S.ScaledGemm(S.make_desc(rows, N, K, out, lda=K, ldb=K, ldd=N, a_scale_strides=p.sa.stride(), b_scale_strides=(kb, 1),
+                                 groups="rows", batch=E, b_stride_l=N * K, b_scale_l=sb.shape[1] * kb))
+    d = torch.empty(rows, N, dtype=OUT[out], device="cuda")
+    h.run(p.a_v, p.sa, b, sb, d, offsets=offsets)
+    at = offsets.tolist()
+    for e in range(E):
+        r = slice(at[e], at[e + 1])
+        if at[e + 1] > at[e]:
+            close(d[r], *reference(p.a[r], p.sa[r], b[e], sb[e], 128, out))
+
+
+def test_every_kernel_is_chosen_somewhere():
+    """The products of this file and the sizes of a decode, a prompt and a training step between
+    them run every kernel."""
+    names = set()
+    for M, N, K, out in ((1, 4096, 4096, "bf16"), (17, 4096, 4096, "bf16"), (32, 16384, 4096, "bf16"), (64, 8192, 4096, "bf16"),
+                         (333, 4096, 8192, "bf16"), (2000, 4096, 1024, "bf16"), (4096, 4096, 4096, "bf16"), (4096, 8192, 1024, "f32"),
+                         (5, 7, 9, "f32")):
+        h = S.ScaledGemm(S.make_desc(M, N, K, out, lda=K, ldb=K, ldd=N, a_scale_strides=(1, M), b_scale_strides=(up(K, 128), 1)))
+        names.add(h.info.name.decode())
+    assert names == {"narrow_64x64", "stream_16x32_w4", "stream_16x16_w8", "stream_32x32_w4", "stream_64x32_w4",
+                     "tile_64x128_w2x2", "tile_128x128_w2x2", "pingpong_256x256"}
