@@ -86,7 +86,9 @@ __global__ __launch_bounds__(1024) void route_hist(const RParams p) {
 // A stable counting sort.  Each workgroup places its chunk of the assignments, each wave a run of
 // it in order: an assignment's row is the expert's first row, plus the expert's assignments in
 // earlier chunks (from route_hist), in earlier waves (counted here first), and in earlier steps
-// and lanes of its wave.  One chunk needs no route_hist.
+// and lanes of its wave.  One chunk needs no route_hist.  131072 assignments to 256 experts: 3.5 +
+// 11 us, the dependent steps of a wave (histogram loads, two passes over LDS, scattered writes); 2048
+// assignments a workgroup and 1024 are alike, 4096 costs 3 us more.
 __global__ __launch_bounds__(1024) void route_place(const RParams p) {
   extern __shared__ int sh[];       // [waves][experts] then, for the scan, one int per wave
   __shared__ int sums[kRouteWaves];
@@ -317,6 +319,9 @@ __device__ __forceinline__ void finish_loss(const BParams& p, int blocks) {
   }
 }
 
+// 16384 x 256 fp32: sums 8 us, finish 10 us (256 KB read by one workgroup; fewer, larger partial sums
+// cost the sums more than they save here), slopes 13 us.
+//
 // Sums of the probabilities over each workgroup's tokens: a wave takes every 16th of them.
 template <int T, int NE>
 __global__ __launch_bounds__(kLossWaves * 64) void balance_sums(const BParams p) {

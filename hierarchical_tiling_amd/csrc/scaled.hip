@@ -52,12 +52,13 @@ hipError_t go_pp(const SParams& p, dim3 grid, hipStream_t s) {
   return hipGetLastError();
 }
 
-#define HT_TILE(NAME, BM, BN, WM, WN, ST, OCC, ...)                                                    \
-  {NAME, BM, BN, WM * WN, ST * (BM + BN) * 132, __VA_ARGS__,                                             \
+#define HT_TILE(NAME, BM, BN, WM, WN, ST, OCC, ...)                                               \
+  {NAME, BM, BN, WM * WN, ST * (BM + BN) * 132, __VA_ARGS__,                                      \
    {{&go_tile<BM, BN, WM, WN, ST, OCC, 128, u16>, &go_tile<BM, BN, WM, WN, ST, OCC, 128, float>}, \
     {&go_tile<BM, BN, WM, WN, ST, OCC, 1, u16>, &go_tile<BM, BN, WM, WN, ST, OCC, 1, float>}}}
-#define HT_STREAM(NAME, RM, NBW, WK, R, OCC, ...)                                                      \
-  {NAME, 16 * RM, 16 * NBW, WK, WK * R * (16 * (RM + NBW) * 128 + (16 * (RM + NBW) + 63) / 64 * 256), __VA_ARGS__, \
+#define HT_STREAM(NAME, RM, NBW, WK, R, OCC, ...)                                                 \
+  {NAME, 16 * RM, 16 * NBW, WK,                                                                   \
+   WK * R * (16 * (RM + NBW) * 128 + (16 * (RM + NBW) + 63) / 64 * 256), __VA_ARGS__,             \
    {{&go_stream<RM, NBW, WK, R, OCC, 128, u16>, &go_stream<RM, NBW, WK, R, OCC, 128, float>},     \
     {&go_stream<RM, NBW, WK, R, OCC, 1, u16>, &go_stream<RM, NBW, WK, R, OCC, 1, float>}}}
 
@@ -110,10 +111,11 @@ double expected_row_tiles(const gemm_scaled_s& h, int bm) {
 
 // Predicted microseconds of a variant with k in `split` slices: rounds of workgroups at the
 // measured cost of a block, against the time that the operands' bytes take at 5.2 TB/s (the less of
-// the two counts a quarter: they overlap, not fully), plus the second kernel of a split.  Over 45
-// measured products and groups the choice by it was the fastest variant or within 12 % of it but
-// for two (17 and 20 %); a rule on rows alone (streaming kernels up to 64 rows, k split until 512
-// workgroups) cost up to 2.3 times the fastest (1000 rows over 32 experts: 141 against 61 us).
+// the two counts a quarter: they overlap, not fully), plus the second kernel of a split.  Over 58
+// measured products and groups (1 to 8192 rows, 300 to 16384 columns, both output types) the choice
+// was on average 2 % above the fastest variant, 57 of them within 12 %, the worst 22 % (3000 x 3000
+// x 512); a rule on rows alone (streaming kernels up to 64 rows, k split until 512 workgroups) cost
+// up to 2.3 times the fastest (1000 rows over 32 experts: 141 against 61 us).
 double predict(const gemm_scaled_s& h, const Variant& v, int split) {
   const gemm_scaled_desc& d = h.d;
   const Cost& c = v.cost;

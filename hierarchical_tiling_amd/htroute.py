@@ -5,6 +5,7 @@ the current device; shapes and types that do not fit raise GemmError.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import htgemm
 from .htgemm import GEMM_ERR_INVALID_ARG, GemmError, _check
@@ -52,13 +53,6 @@ def lib():
     return _lib
 
 
-def workspace_size(tokens, topk, experts) -> int:
-    """Bytes of workspace that route() and balance_loss() need."""
-    n = ctypes.c_size_t()
-    _check(lib().route_workspace_size(tokens, topk, experts, ctypes.byref(n)), "route_workspace_size")
-    return n.value
-
-
 def _bad(what):
     return GemmError(GEMM_ERR_INVALID_ARG, what)
 
@@ -77,14 +71,18 @@ def _mask(mask, tokens, what):
     return mask.data_ptr()
 
 
+@functools.lru_cache(maxsize=64)
+def workspace_size(tokens, topk, experts) -> int:
+    """Bytes of workspace that route() and balance_loss() need."""
+    n = ctypes.c_size_t()
+    _check(lib().route_workspace_size(tokens, topk, experts, ctypes.byref(n)), "route_workspace_size")
+    return n.value
+
+
 def _room(workspace, tokens, topk, experts, what):
     """Address of a workspace of the size these need."""
-    if workspace is None:
+    if workspace is None or workspace.numel() * workspace.element_size() < workspace_size(tokens, topk, experts):
         raise _bad(what)
-    n = ctypes.c_size_t()
-    rc = (_lib or lib()).route_workspace_size(tokens, topk, experts, ctypes.byref(n))
-    if rc or workspace.numel() * workspace.element_size() < n.value:
-        raise GemmError(rc or GEMM_ERR_INVALID_ARG, what)
     return workspace.data_ptr()
 
 
@@ -118,7 +116,7 @@ def route(ids, counts, offsets, order=None, slot=None, mask=None, align=1, works
     dev, stream = _here(stream)
     if _elsewhere(dev, ids, counts, offsets, order, slot, mask, workspace):
         raise _bad("route")
-    rc = _lib.route_experts(ctypes.byref(a), stream)
+    rc = (_lib or lib()).route_experts(ctypes.byref(a), stream)
     if rc:
         raise GemmError(rc, "route_experts")
 
@@ -147,7 +145,7 @@ def balance_loss(logits, counts, topk, loss, prob, live, mask=None, coef=1.0, wo
     dev, stream = _here(stream)
     if _elsewhere(dev, logits, counts, loss, prob, live, mask, workspace):
         raise _bad("balance_loss")
-    rc = _lib.balance_loss(ctypes.byref(a), stream)
+    rc = (_lib or lib()).balance_loss(ctypes.byref(a), stream)
     if rc:
         raise GemmError(rc, "balance_loss")
 
