@@ -9,7 +9,7 @@ import functools
 
 from . import htgemm
 from .htgemm import GEMM_ERR_INVALID_ARG, GemmError, _check
-from .htscaled import _elsewhere, _here, type_code
+from .htscaled import _elsewhere, _here, pitch, type_code
 
 _i32, _i64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
 
@@ -103,14 +103,14 @@ def route(ids, counts, offsets, order=None, slot=None, mask=None, align=1, works
     if ids.dim() != 2 or ids.dtype is not _i32t:
         raise _bad("route")
     tokens, topk = ids.shape
-    step, one = ids.stride()
+    step = pitch(ids, tokens, topk)
     experts = counts.numel()
     rows = 0 if order is None else order.numel()
-    if ((one != 1 and topk > 1) or not _is(counts, _i32t, experts) or not _is(offsets, _i32t, experts + 1) or
+    if (step < 0 or not _is(counts, _i32t, experts) or not _is(offsets, _i32t, experts + 1) or
             (slot is not None and not _is(slot, _i32t, tokens * topk)) or
             (order is not None and not _is(order, _i32t, rows))):
         raise _bad("route")
-    a = route_args(ids.data_ptr(), _mask(mask, tokens, "route"), tokens, step if step > topk else topk, topk, experts,
+    a = route_args(ids.data_ptr(), _mask(mask, tokens, "route"), tokens, step, topk, experts,
                    align, counts.data_ptr(), offsets.data_ptr(), None if order is None else order.data_ptr(), rows,
                    None if slot is None else slot.data_ptr(), _room(workspace, tokens, topk, experts, "route"))
     dev, stream = _here(stream)
@@ -127,10 +127,10 @@ def _logits(logits, counts, what):
     if logits.dim() != 2:
         raise _bad(what)
     tokens, experts = logits.shape
-    step, one = logits.stride()
-    if (one != 1 and experts > 1) or not _is(counts, _i32t, experts):
+    step = pitch(logits, tokens, experts)
+    if step < 0 or not _is(counts, _i32t, experts):
         raise _bad(what)
-    return tokens, experts, step if step > experts else experts
+    return tokens, experts, step
 
 
 def balance_loss(logits, counts, topk, loss, prob, live, mask=None, coef=1.0, workspace=None, stream=None):
@@ -156,12 +156,12 @@ def balance_grad(logits, counts, topk, live, d_loss, d_logits, mask=None, coef=1
     tokens, experts, ld = _logits(logits, counts, "balance_grad")
     if d_logits.shape != logits.shape or d_logits.dtype is not logits.dtype:
         raise _bad("balance_grad")
-    step, one = d_logits.stride()
-    if (one != 1 and experts > 1) or not (_is(live, _i32t, 1) and _is(d_loss, _f32t, 1)):
+    step = pitch(d_logits, tokens, experts)
+    if step < 0 or not (_is(live, _i32t, 1) and _is(d_loss, _f32t, 1)):
         raise _bad("balance_grad")
     a = balance_grad_args(logits.data_ptr(), type_code(logits), experts, topk, coef, tokens, ld,
                           _mask(mask, tokens, "balance_grad"), counts.data_ptr(), live.data_ptr(), d_loss.data_ptr(),
-                          d_logits.data_ptr(), step if step > experts else experts)
+                          d_logits.data_ptr(), step)
     dev, stream = _here(stream)
     if _elsewhere(dev, logits, counts, live, d_loss, d_logits, mask):
         raise _bad("balance_grad")

@@ -170,14 +170,21 @@ def type_code(t) -> int:
     return _TYPE_CODES.get(t.dtype, -1)
 
 
+def pitch(t, rows, cols):
+    """Row stride of a rows x cols tensor with contiguous rows of their own; -1 of any other (rows
+    that overlap, as an expanded tensor's do, among them)."""
+    step, one = t.stride()
+    if one != 1 and cols > 1:
+        return -1
+    return step if step >= cols else cols if rows <= 1 else -1
+
+
 def _codes(t, rows, cols):
     """(address, row stride) of a rows x cols tensor of bytes with contiguous rows; None: another."""
     if t.shape != (rows, cols) or t.element_size() != 1:
         return None
-    step, one = t.stride()
-    if one != 1 and cols > 1:
-        return None
-    return t.data_ptr(), step if step > cols else cols
+    step = pitch(t, rows, cols)
+    return None if step < 0 else (t.data_ptr(), step)
 
 
 def _scale(t, rows, cols):
@@ -202,7 +209,7 @@ def quantize(x, q=None, scale=None, qt=None, scale_t=None, block_rows=1, pow2=Fa
     ok = x.dim() == 2
     if ok:
         x_rows, cols = x.shape
-        step, one = x.stride()
+        step = pitch(x, x_rows, cols)
         rows, index = x_rows, None
         if row_index is not None:
             rows, index = row_index.numel(), row_index.data_ptr()
@@ -212,10 +219,10 @@ def quantize(x, q=None, scale=None, qt=None, scale_t=None, block_rows=1, pow2=Fa
         qt_at = _NO_CODES if qt is None else _codes(qt, cols, rows)
         s_at = _NO_SCALE if scale is None else _scale(scale, rows if block_rows == 1 else rb, cb)
         st_at = _NO_SCALE if scale_t is None else _scale(scale_t, cols, rb)
-        ok = ok and (one == 1 or cols <= 1) and q_at and qt_at and s_at and st_at
+        ok = ok and step >= 0 and q_at and qt_at and s_at and st_at
     if not ok:
         raise GemmError(GEMM_ERR_INVALID_ARG, "quantize")
-    a = quant_args(x.data_ptr(), code, block_rows, pow2, index_div, rows, cols, step if step > cols else cols, index,
+    a = quant_args(x.data_ptr(), code, block_rows, pow2, index_div, rows, cols, step, index,
                    x_rows, *q_at, *s_at, *qt_at, *st_at, pad)
     dev, stream = _here(stream)
     if _elsewhere(dev, x, q, scale, qt, scale_t, row_index):

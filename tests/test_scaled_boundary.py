@@ -194,10 +194,24 @@ def test_shapes_that_do_not_fit():
     for kw in bad:
         with pytest.raises(H.GemmError):
             S.quantize(x, stream=0, **kw)
+    wide = torch.zeros(256).expand(4, 256)    # rows that overlap: a row stride of 0
+    for x2, kw in ((wide, dict(q=q, scale=s)), (x, dict(q=torch.zeros(256, dtype=torch.uint8).expand(4, 256), scale=s)),
+                   (x.t(), dict(q=torch.zeros(256, 4, dtype=torch.uint8), scale=torch.zeros(256, 1)))):
+        with pytest.raises(H.GemmError):
+            S.quantize(x2, stream=0, **kw)
     i = dict(dtype=torch.int32)
+    counts, live, one = torch.zeros(8, **i), torch.zeros(1, **i), torch.zeros(1)
+    ws = torch.zeros(1 << 14, dtype=torch.uint8)
+    with pytest.raises(H.GemmError):
+        R.balance_loss(torch.zeros(8).expand(4, 8), counts, 2, one, torch.zeros(8), live, workspace=ws, stream=0)
+    for x2, d in ((torch.zeros(8).expand(4, 8), torch.zeros(4, 8)), (torch.zeros(4, 8), torch.zeros(8).expand(4, 8)),
+                  (torch.zeros(4, 8), torch.zeros(4, 8).double())):
+        with pytest.raises(H.GemmError):
+            R.balance_grad(x2, counts, 2, live, one, d, stream=0)
     ok = dict(ids=torch.zeros(4, 2, **i), counts=torch.zeros(8, **i), offsets=torch.zeros(9, **i),
               workspace=torch.zeros(1 << 14, dtype=torch.uint8))
-    for kw in (dict(ids=torch.zeros(4, 2)), dict(offsets=torch.zeros(8, **i)), dict(counts=torch.zeros(8)),
+    for kw in (dict(ids=torch.zeros(4, 2)), dict(ids=torch.zeros(2, **i).expand(4, 2)),
+               dict(offsets=torch.zeros(8, **i)), dict(counts=torch.zeros(8)),
                dict(slot=torch.zeros(4, 1, **i)), dict(mask=torch.zeros(3, dtype=torch.uint8)), dict(workspace=None),
                dict(workspace=torch.zeros(1, dtype=torch.uint8)), dict(mask=torch.zeros(4))):
         with pytest.raises(H.GemmError):
