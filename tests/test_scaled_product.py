@@ -78,7 +78,7 @@ def test_shapes(shape, out, b_block):
 
 
 @pytest.mark.parametrize("shape", [(1, 4096, 2048), (5, 8192, 512), (40, 4096, 1024), (64, 2048, 256),
-                                   (300, 4096, 256), (4096, 4096, 256), (4000, 4100, 272)])
+                                   (300, 4096, 256), (4096, 4096, 256), (4000, 4100, 272), (4099, 4097, 1040)])
 @pytest.mark.parametrize("out,b_block", [("bf16", 128), ("f32", 1), ("bf16", 1), ("f32", 128)])
 def test_wide(shape, out, b_block):
     Problem(*shape, out=out, b_block=b_block, seed=1).check(act="silu", bias=True)
@@ -312,10 +312,13 @@ def test_refusals_at_run():
     h.close()
 
 
-@pytest.mark.parametrize("rows,E,N,K", [(3000, 6, 640, 512), (700, 300, 96, 256), (2600, 3, 300, 400)])
-@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,E,N,K,out", [
+    (3000, 6, 640, 512, "bf16"), (700, 300, 96, 256, "bf16"), (2600, 3, 300, 400, "bf16"),
+    (3000, 6, 640, 512, "f32"), (700, 300, 96, 256, "f32"), (2600, 3, 300, 400, "f32"),
+    (8190, 32, 4096, 2048, "bf16")])
 def test_many_groups_and_large_groups(rows, E, N, K, out):
-    """Groups of more than a tile's rows, and more groups than lanes, against the product of each."""
+    """Groups of more than a tile's rows, and more groups than lanes, against the product of each;
+    the last through the ping-pong kernel."""
     g = gen(rows)
     p = Problem(rows, N, K, out=out, seed=rows, spread=1.0)
     to = torch.sort(torch.randint(0, E, (rows,), generator=g, device="cuda")).values
@@ -326,6 +329,7 @@ def test_many_groups_and_large_groups(rows, E, N, K, out):
     sb = scales(g, E, up(N, BLOCK), kb)
     h = S.ScaledGemm(S.make_desc(rows, N, K, out, lda=K, ldb=K, ldd=N, a_scale_strides=p.sa.stride(), b_scale_strides=(kb, 1),
                                  groups="rows", batch=E, b_stride_l=N * K, b_scale_l=sb.shape[1] * kb))
+    assert (h.info.name == b"pingpong_256x256") == (rows == 8190)
     d = torch.empty(rows, N, dtype=OUT[out], device="cuda")
     h.run(p.a_v, p.sa, b, sb, d, offsets=offsets)
     at = offsets.tolist()
