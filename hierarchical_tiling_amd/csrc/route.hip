@@ -10,6 +10,8 @@ namespace {
 
 constexpr int kRouteWaves = 16, kRouteChunk = 2048, kRouteBlocks = 256;
 constexpr int kLossWaves = 16, kLossBlocks = 256;
+constexpr int kFinishExperts = 16;
+constexpr int kLossHead = 64 * 8 + 16;   // bytes of dots and ticket before the workgroups' sums
 
 // ---- order ---------------------------------------------------------------------------------
 struct RParams {
@@ -29,8 +31,8 @@ struct RParams {
 };
 
 // The expert of assignment i, or -1 when it is dropped.  The division is one multiplication:
-// floor(i / k) = floor(i * ceil(2^36 / k) / 2^36) for i < 2^30 and k <= 64, since the excess of the
-// rounded factor, below i / 2^36 < 1 / 64, is less than the 1 / k to the next whole number.
+// floor(i / k) = floor(i * ceil(2^s / k) / 2^s) for i < 2^30 and 2^(s - 30) >= k, since the excess of
+// the rounded factor, below i / 2^s < 1 / k, is less than the 1 / k to the next whole number.
 __device__ __forceinline__ int expert_of(const RParams& p, int i) {
   const int t = (int)((uint64_t)i * p.topk_inverse >> p.topk_shift);
   if (p.mask && !p.mask[t]) return -1;
@@ -178,6 +180,8 @@ struct BParams {
   int64_t tokens, ld, ld_d;
   int experts, topk;
   float coef;
+  double* dots;        // parts of the loss, one for each kFinishExperts experts
+  int32_t* ticket;
   float* partial;      // blocks x experts
   int32_t* partial_n;  // blocks
   float* loss;
@@ -266,61 +270,13 @@ __device__ __forceinline__ int softmax_rows(const BParams& p, int64_t t, int64_t
   return bits;
 }
 
-// prob and loss from the workgroups' sums, added in a fixed order, in double: thread (g, quad) takes
-// four experts of every G-th workgroup, then the G sums of an expert are added.
-template <int NT>
-__device__ __forceinline__ void finish_loss(const BParams& p, int blocks) {
-  __shared__ double part[NT * 4];
-  __shared__ int n_live;
-  const int tid = threadIdx.x, E = p.experts, quads = (E + 3) / 4, G = NT / quads;
-  if (tid == 0) n_live = 0;
-  __syncthreads();
-  int n = 0;
-  for (int b = tid; b < blocks; b += NT) n += p.partial_n[b];
-  const int my_count = tid < E ? p.counts[tid] : 0;   // beside the sums' loads, not behind them
-  const int g = tid / quads, e0 = (tid - g * quads) * 4;
-  if (g < G) {
-    double s[4] = {0.0, 0.0, 0.0, 0.0};
-    if (E % 4 == 0) {
-#pragma unroll 16
-      for (int b = g; b < blocks; b += G) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(p.partial + (int64_t)b * E + e0);
-        static_for<4>([&](auto i) { s[i] += v[(int)i]; });
-      }
-    } else {
-#pragma unroll 4
-      for (int b = g; b < blocks; b += G)
-        static_for<4>([&](auto i) { s[i] += e0 + i < E ? p.partial[(int64_t)b * E + e0 + i] : 0.f; });
-    }
-    static_for<4>([&](auto i) { part[g * quads * 4 + e0 + i] = s[i]; });
-  }
-  if (n) atomicAdd(&n_live, n);     // integers: any order gives the same sum
-  __syncthreads();
-  n = n_live;
-  double dot = 0.0;
-  static_assert(NT >= ROUTE_MAX_EXPERTS, "a thread for each expert");
-  if (tid < E) {
-    double s = 0.0;
-    for (int q = 0; q < G && q < blocks; ++q) s += part[q * quads * 4 + tid];
-    const double mean = n > 0 ? s / n : 0.0;
-    p.prob[tid] = (float)mean;
-    dot = mean * my_count;
-  }
-  __syncthreads();
-  part[tid] = dot;
-  __syncthreads();
-  if (tid < 64) {
-    for (int w = 1; w < NT / 64; ++w) dot += part[w * 64 + tid];
-    for (int d = 32; d > 0; d >>= 1) dot += __shfl_xor(dot, d, 64);
-  }
-  if (tid == 0) {
-    *p.loss = n > 0 ? (float)(p.coef * dot * E / ((double)p.topk * n)) : 0.f;
-    *p.live = n;
-  }
+// loss and live from dot = sum over the experts of mean probability x count and the n rows that count
+__device__ __forceinline__ void put_loss(const BParams& p, double dot, int n) {
+  *p.loss = n > 0 ? (float)(p.coef * dot * p.experts / ((double)p.topk * n)) : 0.f;
+  *p.live = n;
 }
 
-// 16384 x 256 fp32: sums 8 us, finish 10 us (256 KB read by one workgroup; fewer, larger partial sums
-// cost the sums more than they save here), slopes 13 us.
+// 16384 x 256 fp32: sums 8 us, finish 5 us, slopes 13 us.
 //
 // Sums of the probabilities over each workgroup's tokens: a wave takes every 16th of them.
 template <int T, int NE>
@@ -343,24 +299,90 @@ __global__ __launch_bounds__(kLossWaves * 64) void balance_sums(const BParams p)
   });
   if (lane == 0) live[wave] = n;
   __syncthreads();
-  for (int e = tid; e < p.experts; e += kLossWaves * 64) {
-    float s = 0.f;
-    for (int w = 0; w < kLossWaves; ++w) s += sums[w * p.experts + e];
-    p.partial[(int64_t)blockIdx.x * p.experts + e] = s;
+  static_assert(ROUTE_MAX_EXPERTS <= kLossWaves * 64, "a thread for each expert");
+  float s = 0.f;
+  if (tid < p.experts) {
+    for (int w = 0; w < kLossWaves; ++w) s += sums[w * p.experts + tid];
+    if (gridDim.x > 1) p.partial[(int64_t)blockIdx.x * p.experts + tid] = s;
   }
+  n = 0;
+  for (int w = 0; w < kLossWaves; ++w) n += live[w];
+  if (gridDim.x > 1) {
+    if (tid == 0) p.partial_n[blockIdx.x] = n;
+    if (tid == 0 && blockIdx.x == 0) *p.ticket = 0;
+    return;
+  }
+  // one workgroup has all the sums: finish here
+  __shared__ double dots[kLossWaves];
+  double dot = 0.0;
+  if (tid < p.experts) {
+    const double mean = n > 0 ? (double)s / n : 0.0;
+    p.prob[tid] = (float)mean;
+    dot = mean * p.counts[tid];
+  }
+  for (int d = 32; d > 0; d >>= 1) dot += __shfl_xor(dot, d, 64);
+  if (lane == 0) dots[wave] = dot;
+  __syncthreads();
   if (tid == 0) {
-    n = 0;
-    for (int w = 0; w < kLossWaves; ++w) n += live[w];
-    p.partial_n[blockIdx.x] = n;
-  }
-  if (gridDim.x == 1) {             // one workgroup has all the sums: finish here
-    __threadfence_block();
-    __syncthreads();
-    finish_loss<kLossWaves * 64>(p, 1);
+    for (int w = 1; w < kLossWaves; ++w) dot += dots[w];
+    put_loss(p, dot, n);
   }
 }
 
-__global__ __launch_bounds__(1024) void balance_finish(const BParams p, int blocks) { finish_loss<1024>(p, blocks); }
+// prob and loss from the workgroups' sums, added in a fixed order, in double.  A workgroup takes 16
+// experts, so that the sums are read by several (by one: 10 us for 256 KB); thread (g, quad) adds
+// four experts of every 64th sum.  The last workgroup to end, by a ticket that balance_sums has set
+// to zero, adds the workgroups' parts of the loss, in their order.
+__global__ __launch_bounds__(256) void balance_finish(const BParams p, int blocks) {
+  __shared__ double part[4][kFinishExperts];
+  __shared__ int live[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = p.experts;
+  const int quad = tid & 3, first = blockIdx.x * kFinishExperts, e0 = first + quad * 4;
+  int n = tid < blocks ? p.partial_n[tid] : 0;
+  const int count = tid < kFinishExperts && first + tid < E ? p.counts[first + tid] : 0;
+  f32x4 v[kLossBlocks / 64];
+  static_for<kLossBlocks / 64>([&](auto k) {
+    const int b = (tid >> 2) + k * 64;
+    const float* src = p.partial + (int64_t)b * E + e0;
+    v[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (b < blocks) {
+      if (E % 4 == 0) {
+        if (e0 < E) v[k] = *reinterpret_cast<const f32x4*>(src);
+      } else {
+        static_for<4>([&](auto i) { if (e0 + i < E) v[k][(int)i] = src[(int)i]; });
+      }
+    }
+  });
+  static_for<4>([&](auto i) {
+    double s = 0.0;
+    static_for<kLossBlocks / 64>([&](auto k) { s += v[k][(int)i]; });
+    for (int d = 4; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
+    if (lane < 4) part[wave][quad * 4 + i] = s;
+  });
+  for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d, 64);
+  if (lane == 0) live[wave] = n;
+  __syncthreads();
+  if (wave != 0) return;
+  n = live[0] + live[1] + live[2] + live[3];
+  double dot = 0.0;
+  if (lane < kFinishExperts && first + lane < E) {
+    const double s = part[0][lane] + part[1][lane] + part[2][lane] + part[3][lane];
+    const double mean = n > 0 ? s / n : 0.0;
+    p.prob[first + lane] = (float)mean;
+    dot = mean * count;
+  }
+  for (int d = 32; d > 0; d >>= 1) dot += __shfl_xor(dot, d, 64);
+  int last = 0;
+  if (lane == 0) {
+    __hip_atomic_store(p.dots + blockIdx.x, dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last = __hip_atomic_fetch_add(p.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+  }
+  if (!__builtin_amdgcn_readfirstlane(last)) return;
+  static_assert(ROUTE_MAX_EXPERTS <= 64 * kFinishExperts && kLossBlocks == 256, "a lane for each part");
+  dot = lane < (int)gridDim.x ? __hip_atomic_load(p.dots + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+  for (int d = 32; d > 0; d >>= 1) dot += __shfl_xor(dot, d, 64);
+  if (lane == 0) put_loss(p, dot, n);
+}
 
 // g is taken relative to an even load, (experts * counts - topk * n) as an integer: the constant
 // drops out of g - sum p g, and what is left has no cancellation to lose bits to.
@@ -447,7 +469,7 @@ int route_workspace_size(int64_t tokens, int32_t topk, int32_t experts, size_t* 
   if (rc) return rc;
   if (!bytes) return GEMM_ERR_INVALID_ARG;
   const size_t hist = (size_t)route_blocks(tokens * topk) * experts * 4;
-  const size_t loss = (size_t)loss_blocks(tokens) * (experts + 1) * 4;
+  const size_t loss = kLossHead + (size_t)loss_blocks(tokens) * (experts + 1) * 4;
   *bytes = (std::max(hist, loss) + 255) / 256 * 256;
   return GEMM_OK;
 }
@@ -515,7 +537,9 @@ int balance_loss(const balance_args* a, void* stream) {
   p.experts = a->experts;
   p.topk = a->topk;
   p.coef = a->coef;
-  p.partial = static_cast<float*>(a->workspace);
+  p.dots = static_cast<double*>(a->workspace);
+  p.ticket = reinterpret_cast<int32_t*>(p.dots + 64);
+  p.partial = reinterpret_cast<float*>(p.dots + kLossHead / 8);
   p.partial_n = reinterpret_cast<int32_t*>(p.partial + blocks * a->experts);
   p.loss = a->loss;
   p.prob = a->prob;
@@ -530,7 +554,8 @@ int balance_loss(const balance_args* a, void* stream) {
   });
   if (hipGetLastError() != hipSuccess) return GEMM_ERR_LAUNCH;
   if (blocks > 1) {
-    hipLaunchKernelGGL(balance_finish, dim3(1), dim3(1024), 0, s, p, (int)blocks);
+    const unsigned parts = (unsigned)((a->experts + kFinishExperts - 1) / kFinishExperts);
+    hipLaunchKernelGGL(balance_finish, dim3(parts), dim3(256), 0, s, p, (int)blocks);
     if (hipGetLastError() != hipSuccess) return GEMM_ERR_LAUNCH;
   }
   return GEMM_OK;
