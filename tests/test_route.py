@@ -145,7 +145,8 @@ def check(logits, counts, topk, mask=None, coef=0.01, d_loss=1.0):
 
 
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 4, 2), (37, 64, 6), (3, 65, 2), (64, 100, 4), (500, 256, 8),
-                                   (257, 130, 2), (300, 512, 8), (70, 1000, 3), (8000, 16, 2)])
+                                   (257, 130, 2), (300, 512, 8), (70, 1000, 3), (8000, 16, 2),
+                                   (70, 992, 3), (65, 1024, 8), (300, 204, 4), (9, 66, 1)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
 def test_balance(T, E, k, dtype):
     g = torch.Generator(device="cuda")
