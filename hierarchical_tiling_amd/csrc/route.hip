@@ -227,7 +227,7 @@ template <bool MAX> __device__ __forceinline__ float wave_all(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
-// Rows a wave has in hand at once, so that their loads and reductions overlap.
+// Rows a wave of balance_sums has in hand at once, so that their loads and reductions overlap.
 template <int NE> constexpr int rows_at_once() { return NE >= 16 ? 2 : 4; }
 
 // Softmax of R rows t, t + step, ... below `end`, lane l holding experts l, l + 64, ...; zero in all
@@ -276,7 +276,7 @@ __device__ __forceinline__ void put_loss(const BParams& p, double dot, int n) {
   *p.live = n;
 }
 
-// 16384 x 256 fp32: sums 8 us, finish 5 us, slopes 13 us.
+// 16384 x 256 fp32: sums 8 us, finish 5 us, slopes 12 us.
 //
 // Sums of the probabilities over each workgroup's tokens: a wave takes every 16th of them.
 template <int T, int NE>
@@ -398,7 +398,7 @@ __global__ __launch_bounds__(256) void balance_slopes(const BParams p) {
     const int e = lane + 64 * i;
     g[i] = e < p.experts ? scale * (float)((int64_t)p.counts[e] * p.experts - (int64_t)p.topk * n) : 0.f;
   });
-  constexpr int R = rows_at_once<NE>();
+  constexpr int R = 2;   // with 2048 workgroups; half of them and 4 rows a wave: 1 us more
   for (int64_t t = w; t < p.tokens; t += R * waves) {
     float v[R][NE];
     const int live = softmax_rows<T, NE, R>(p, t, waves, p.tokens, lane, v);
@@ -585,7 +585,7 @@ int balance_grad(const balance_grad_args* a, void* stream) {
   p.live = const_cast<int32_t*>(a->live);
   p.d_loss = a->d_loss;
   p.d_logits = a->d_logits;
-  const unsigned blocks = (unsigned)std::min<int64_t>((a->tokens + 3) / 4, 1024);
+  const unsigned blocks = (unsigned)std::min<int64_t>((a->tokens + 3) / 4, 2048);
   hipStream_t s = (hipStream_t)stream;
   with_type(a->type, [&](auto T) {
     with_lanes(a->experts, [&](auto NE) {
