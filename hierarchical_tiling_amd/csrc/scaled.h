@@ -457,20 +457,25 @@ typedef __attribute__((address_space(1))) const void gbl_void_t;
 //
 // Rows are placed in LDS so that a lane's rows are neighbours: LDS row i * 16 + x of a wave's A
 // tile is its row x * RM + i, and LDS row j * 16 + y of its B tile the column that Cols gives.  The
-// lane's A scales are then contiguous in LDS, and its outputs in D.  The placement costs nothing: every DMA lane has its
-// own source address.
+// lane's A scales are then contiguous in LDS, and its outputs in D.  The placement costs nothing:
+// every DMA lane has its own source address.
 //
 // Measured, two workgroups a CU: bf16 out 0.55 us for a block of a 128 x 128 tile and 0.36 us for one
 // of 64 x 128 (8192^3: 560 and 738 us), where LDS traffic and the barrier bound it; with one
-// workgroup a CU 0.72 and 0.43 (333 x 4096 x 8192: 31 us).  fp32 out 1.0 us (4096 x 8192 x 5120 with
-// scales of single columns: 330 us, 1,040 TFLOP/s) is bound by issue: a wave's block of 64 x 64 has
-// 64 matrix instructions of 8 issue cycles, 128 conversions and 128 scale operations of 4.  Two
-// workgroups of 4 waves hide each other's phases; one workgroup with four stages took 737 us.
-// Reading fragments a block ahead, six stages, and 2 or 8 waves for the same tile changed nothing or
-// lost.
+// workgroup a CU 0.72 and 0.43.  fp32 out 1.0 us (4096 x 8192 x 5120 with scales of single columns:
+// 330 us, 1,040 TFLOP/s) is bound by issue: a wave's block of 64 x 64 has 64 matrix instructions of
+// 8 issue cycles, 128 conversions and 128 scale operations of 4.  Two workgroups of 4 waves hide each
+// other's phases; one workgroup with four stages took 737 us.  Reading fragments a block ahead, six
+// stages, and 2 or 8 waves that share one block of the same tile changed nothing or lost.
+//
+// KH = 2, for fewer tiles than two a CU: two halves of the waves take the even and the odd blocks of
+// k, each through a ring of its own, and join in LDS at the end.  They overlap as two workgroups
+// would, without a split's planes in memory: 333 x 4096 x 8192 33 -> 29 us (fp32 48 -> 43), 1000 x
+// 4096 x 4096 with 128 x 128 tiles 29 -> 26.  With more tiles two workgroups a CU overlap their
+// prologues and epilogues too (128 rows over 64 experts 80 us, with halves 95).
 // ------------------------------------------------------------------------------------------
-template <int BM, int BN, int WM, int WN, int ST, int BB, class OT, int OCC>
-__global__ __launch_bounds__(WM * WN * 64, OCC) void scaled_tile(const SParams p) {
+template <int BM, int BN, int WM, int WN, int ST, int BB, class OT, int OCC, int KH>
+__global__ __launch_bounds__(KH * WM * WN * 64, OCC) void scaled_tile(const SParams p) {
   constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, RM = TM / 16, RN = TN / 16;
   constexpr int OPS_T = (BM + BN) / 8 / NW;          // tile DMA instructions per wave and block
   constexpr int SCI = (BM + BN) / 64;                // scale DMA instructions per block
@@ -479,11 +484,13 @@ __global__ __launch_bounds__(WM * WN * 64, OCC) void scaled_tile(const SParams p
   constexpr int STAGE = (BM + BN) * 8 + (BM + BN) / 4;  // 16-byte chunks
   static_assert((BM + BN) % (8 * NW) == 0 && BM % 64 == 0 && BN % 64 == 0, "DMA blocks over the waves");
   static_assert(TN <= kSB && kSB % TN == 0, "one 128-wide B scale per wave");
-  __shared__ u32x4 lds[ST * STAGE];
+  __shared__ u32x4 lds[KH * ST * STAGE];
   STile s;
   if (!tile_share<BM, BN, OT>(p, s)) return;
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = KH == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid / (NW * 64));
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) - half * NW;
+  u32x4* ring = lds + half * ST * STAGE;
   const int wm = wave / WN, wn = wave % WN;
   const int x = lane & 15, g = lane >> 4;
 
@@ -525,11 +532,12 @@ __global__ __launch_bounds__(WM * WN * 64, OCC) void scaled_tile(const SParams p
       sc_step[i] = p.b_sk;
     }
   });
-  // Blocks past the last are issued as zeros, so that the wait counts are the same throughout.
+  // Step t of a half is block t KH + half.  Blocks past the last are issued as zeros, so that the wait counts are the same throughout.
   auto dma = [&](int t, int stage) {
-    u32x4* st = lds + stage * STAGE;
+    u32x4* st = ring + stage * STAGE;
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(a_tile, a_span), rb = make_rsrc(b_tile, b_span);
-    const int64_t k = (int64_t)t * kSB;
+    const int b = t * KH + half;
+    const int64_t k = (int64_t)b * kSB;
     const bool in_k = k + chunk * 16 < K;
     static_for<OPS_T>([&](auto i) {
       const int blk = wave + NW * i;
@@ -541,7 +549,7 @@ __global__ __launch_bounds__(WM * WN * 64, OCC) void scaled_tile(const SParams p
     });
     static_for<OPS_S>([&](auto i) {
       const int ins = (wave + NW * i) % SCI;
-      const float* src = sc_ptr[i] + (int64_t)min(t, nk - 1) * sc_step[i];
+      const float* src = sc_ptr[i] + (int64_t)min(b, nk - 1) * sc_step[i];
       __builtin_amdgcn_global_load_lds((gbl_void_t*)src, (lds_void_t*)(st + (BM + BN) * 8 + ins * 16), 4, 0, 0);
     });
   };
@@ -552,7 +560,7 @@ __global__ __launch_bounds__(WM * WN * 64, OCC) void scaled_tile(const SParams p
   static_for<2>([&](auto u) { slot[u] = swizzled_slot<8>(x, g + 4 * u); });
 
   auto compute = [&](int stage) {
-    const u32x4* st = lds + stage * STAGE;
+    const u32x4* st = ring + stage * STAGE;
     const u32x4* la = st + wm * TM * 8;
     const u32x4* lb = st + (BM + wn * TN) * 8;
     const float* ls = reinterpret_cast<const float*>(st + (BM + BN) * 8);
@@ -584,7 +592,7 @@ __global__ __launch_bounds__(WM * WN * 64, OCC) void scaled_tile(const SParams p
   if (nk > 0) {
     static_for<ST - 1>([&](auto q) { dma(q, q); });
     int stage = 0;
-    for (int t = 0; t < nk; ++t) {
+    for (int t = 0; t * KH < nk; ++t) {
       // block t has landed for this wave and, behind the barrier, for all; the stage refilled
       // next was last read before it
       wait_counts<(ST - 2) * OPS, true>();
@@ -592,13 +600,21 @@ __global__ __launch_bounds__(WM * WN * 64, OCC) void scaled_tile(const SParams p
       int next = stage + ST - 1;
       if (next >= ST) next -= ST;
       dma(t + ST - 1, next);
-      compute(stage);
+      if (KH == 1 || t * KH + half < nk) compute(stage);
       if (++stage == ST) stage = 0;
     }
     wait_counts<0, true>();  // zero blocks issued past the end
   }
+  if constexpr (KH == 2) {      // the second half's sums are added to the first's, which stores
+    static_assert(NW * RM * RN * 64 <= KH * ST * STAGE, "its sums fit the ring");
+    f32x4* sums = reinterpret_cast<f32x4*>(lds) + wave * RM * RN * 64 + lane;
+    __syncthreads();
+    if (half == 1) static_for<RM>([&](auto i) { static_for<RN>([&](auto j) { sums[(i * RN + j) * 64] = acc[i][j]; }); });
+    __syncthreads();
+    if (half == 0) static_for<RM>([&](auto i) { static_for<RN>([&](auto j) { acc[i][j] += sums[(i * RN + j) * 64]; }); });
+  }
   store_outputs<OT, BN, RM, RN>(p, s, acc, [&](int i, int r) { return s.m0 + wm * TM + r * RM + i; },
-                                s.n0 + wn * TN, lds, wave);
+                                half == 0 ? s.n0 + wn * TN : p.N, lds, wave);
 }
 
 // ------------------------------------------------------------------------------------------

@@ -18,9 +18,10 @@ constexpr int64_t kCUs = 256;
 typedef hipError_t (*scaled_launch)(const SParams&, dim3, hipStream_t);
 
 // One kernel: its tile, its launch for b_block 128 / 1 and bf16 / f32 outputs, and what choose()
-// goes by: workgroups a CU holds at once (occ), waves that share k (kw), microseconds for a block
-// of k while a CU has one workgroup (c1) and while it has occ of them (c2), for bf16 and f32
-// outputs, and for each round of workgroups beside them (round).  Measured on MI355X.
+// goes by: workgroups a CU holds at once (occ), waves (or halves of them) that share k (kw),
+// microseconds for a block of k while a CU has one workgroup (c1) and while it has occ of them (c2),
+// for bf16 and f32 outputs, and for each round of workgroups beside them (round).  Measured on
+// MI355X.
 struct Cost {
   int occ, kw;
   float c1[2], c2[2], round;
@@ -32,9 +33,9 @@ struct Variant {
   scaled_launch launch[2][2];
 };
 
-template <int BM, int BN, int WM, int WN, int ST, int OCC, int BB, class OT>
+template <int BM, int BN, int WM, int WN, int ST, int OCC, int KH, int BB, class OT>
 hipError_t go_tile(const SParams& p, dim3 grid, hipStream_t s) {
-  hipLaunchKernelGGL((scaled_tile<BM, BN, WM, WN, ST, BB, OT, OCC>), grid, dim3(WM * WN * 64), 0, s, p);
+  hipLaunchKernelGGL((scaled_tile<BM, BN, WM, WN, ST, BB, OT, OCC, KH>), grid, dim3(KH * WM * WN * 64), 0, s, p);
   return hipGetLastError();
 }
 template <int RM, int NBW, int WK, int R, int OCC, int BB, class OT>
@@ -52,17 +53,17 @@ hipError_t go_pp(const SParams& p, dim3 grid, hipStream_t s) {
   return hipGetLastError();
 }
 
-#define HT_TILE(NAME, BM, BN, WM, WN, ST, OCC, ...)                                               \
-  {NAME, BM, BN, WM * WN, ST * (BM + BN) * 132, __VA_ARGS__,                                      \
-   {{&go_tile<BM, BN, WM, WN, ST, OCC, 128, u16>, &go_tile<BM, BN, WM, WN, ST, OCC, 128, float>}, \
-    {&go_tile<BM, BN, WM, WN, ST, OCC, 1, u16>, &go_tile<BM, BN, WM, WN, ST, OCC, 1, float>}}}
+#define HT_TILE(NAME, BM, BN, WM, WN, ST, OCC, KH, ...)                                                   \
+  {NAME, BM, BN, KH * WM * WN, KH * ST * (BM + BN) * 132, __VA_ARGS__,                                    \
+   {{&go_tile<BM, BN, WM, WN, ST, OCC, KH, 128, u16>, &go_tile<BM, BN, WM, WN, ST, OCC, KH, 128, float>}, \
+    {&go_tile<BM, BN, WM, WN, ST, OCC, KH, 1, u16>, &go_tile<BM, BN, WM, WN, ST, OCC, KH, 1, float>}}}
 #define HT_STREAM(NAME, RM, NBW, WK, R, OCC, ...)                                                 \
   {NAME, 16 * RM, 16 * NBW, WK,                                                                   \
    WK * R * (16 * (RM + NBW) * 128 + (16 * (RM + NBW) + 63) / 64 * 256), __VA_ARGS__,             \
    {{&go_stream<RM, NBW, WK, R, OCC, 128, u16>, &go_stream<RM, NBW, WK, R, OCC, 128, float>},     \
     {&go_stream<RM, NBW, WK, R, OCC, 1, u16>, &go_stream<RM, NBW, WK, R, OCC, 1, float>}}}
 
-enum { V_NARROW, V_S16, V_S16N, V_S32, V_S64, V_T64, V_T128, V_PP, V_COUNT };
+enum { V_NARROW, V_S16, V_S16N, V_S32, V_S64, V_T64, V_T64K, V_T128, V_T128K, V_PP, V_COUNT };
 #define HT_COST(...) {__VA_ARGS__}
 const Variant kVariants[V_COUNT] = {
     {"narrow_64x64", 64, 64, 4, 16384, {2, 1, {3.f, 3.f}, {6.f, 6.f}, 2.f},
@@ -71,8 +72,10 @@ const Variant kVariants[V_COUNT] = {
     HT_STREAM("stream_16x16_w8", 1, 1, 8, 4, 1, HT_COST(1, 8, {.38f, .40f}, {.38f, .40f}, 2.f)),
     HT_STREAM("stream_32x32_w4", 2, 2, 4, 3, 1, HT_COST(1, 4, {.55f, .65f}, {.55f, .65f}, 3.f)),
     HT_STREAM("stream_64x32_w4", 4, 2, 4, 3, 1, HT_COST(1, 4, {1.0f, 1.2f}, {1.0f, 1.2f}, 3.f)),
-    HT_TILE("tile_64x128_w2x2", 64, 128, 2, 2, 3, 2, HT_COST(2, 1, {.43f, .80f}, {.72f, 1.30f}, 1.5f)),
-    HT_TILE("tile_128x128_w2x2", 128, 128, 2, 2, 2, 2, HT_COST(2, 1, {.72f, 1.25f}, {1.09f, 2.00f}, 1.5f)),
+    HT_TILE("tile_64x128_w2x2", 64, 128, 2, 2, 3, 2, 1, HT_COST(2, 1, {.43f, .80f}, {.72f, 1.30f}, 1.5f)),
+    HT_TILE("tile_64x128_w2x2x2", 64, 128, 2, 2, 3, 1, 2, HT_COST(1, 2, {.72f, 1.30f}, {.72f, 1.30f}, 2.5f)),
+    HT_TILE("tile_128x128_w2x2", 128, 128, 2, 2, 2, 2, 1, HT_COST(2, 1, {.72f, 1.25f}, {1.09f, 2.00f}, 1.5f)),
+    HT_TILE("tile_128x128_w2x2x2", 128, 128, 2, 2, 2, 1, 2, HT_COST(1, 2, {1.09f, 2.00f}, {1.09f, 2.00f}, 3.f)),
     {"pingpong_256x256", 256, 256, 8, 160 * 1024, {1, 1, {1.40f, 0.f}, {1.40f, 0.f}, 6.f},
      {{&go_pp, nullptr}, {nullptr, nullptr}}},
 };
@@ -111,9 +114,9 @@ double expected_row_tiles(const gemm_scaled_s& h, int bm) {
 
 // Predicted microseconds of a variant with k in `split` slices: rounds of workgroups at the
 // measured cost of a block, against the time that the operands' bytes take at 5.2 TB/s (the less of
-// the two counts a quarter: they overlap, not fully), plus the second kernel of a split.  Over 58
+// the two counts a quarter: they overlap, not fully), plus the second kernel of a split.  Over 74
 // measured products and groups (1 to 8192 rows, 300 to 16384 columns, both output types) the choice
-// was on average 2 % above the fastest variant, 57 of them within 12 %, the worst 22 % (3000 x 3000
+// was on average 2 % above the fastest variant, 72 of them within 12 %, the worst 22 % (3000 x 3000
 // x 512); a rule on rows alone (streaming kernels up to 64 rows, k split until 512 workgroups) cost
 // up to 2.3 times the fastest (1000 rows over 32 experts: 141 against 61 us).
 double predict(const gemm_scaled_s& h, const Variant& v, int split) {

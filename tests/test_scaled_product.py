@@ -84,6 +84,19 @@ def test_wide(shape, out, b_block):
     Problem(*shape, out=out, b_block=b_block, seed=1).check(act="silu", bias=True)
 
 
+@pytest.mark.parametrize("shape,tile", [((333, 4096, 4224), 64), ((257, 5000, 3984), 64), ((130, 7168, 4112), 64),
+                                        ((1000, 4096, 3984), 128), ((1000, 3900, 4112), 128),
+                                        # near the sizes where another kernel is chosen
+                                        ((130, 7168, 2064), 0), ((257, 8000, 1936), 0), ((2000, 2100, 2192), 0)])
+@pytest.mark.parametrize("out,b_block", [("bf16", 128), ("f32", 1), ("bf16", 1), ("f32", 128)])
+def test_two_halves_of_k(shape, tile, out, b_block):
+    """Odd and even numbers of blocks, whole and partial last ones, between the two halves of the
+    waves; with C, an activation and bias, and for whole and ragged columns."""
+    p = Problem(*shape, out=out, b_block=b_block, seed=3, spread=1.0)
+    h = p.check(act="gelu", bias=True, row_scale=True, alpha=0.5, beta=0.25)
+    assert not tile or h.info.name.decode() == f"tile_{tile}x128_w2x2x2"
+
+
 @pytest.mark.parametrize("shape", [(1, 1, 1), (2, 3, 127), (7, 9, 129), (70, 65, 300), (16, 64, 1001)])
 @pytest.mark.parametrize("off,pad", [(0, 0), (1, 0), (0, 5), (3, 16)])
 def test_any_alignment(shape, off, pad):
@@ -343,10 +356,11 @@ def test_every_kernel_is_chosen_somewhere():
     """The products of this file and the sizes of a decode, a prompt and a training step between
     them run every kernel."""
     names = set()
-    for M, N, K, out in ((1, 4096, 4096, "bf16"), (17, 4096, 4096, "bf16"), (32, 16384, 4096, "bf16"), (64, 8192, 4096, "bf16"),
-                         (333, 4096, 8192, "bf16"), (2000, 4096, 1024, "bf16"), (4096, 4096, 4096, "bf16"), (4096, 8192, 1024, "f32"),
-                         (5, 7, 9, "f32")):
+    for M, N, K, out in ((1, 4096, 4096, "bf16"), (17, 4096, 4096, "bf16"), (32, 8192, 8192, "bf16"), (64, 8192, 4096, "bf16"),
+                         (333, 4096, 8192, "bf16"), (1000, 4096, 512, "bf16"), (1000, 4096, 4096, "bf16"),
+                         (2000, 4096, 1024, "bf16"), (4096, 4096, 4096, "bf16"), (4096, 8192, 1024, "f32"), (5, 7, 9, "f32")):
         h = S.ScaledGemm(S.make_desc(M, N, K, out, lda=K, ldb=K, ldd=N, a_scale_strides=(1, M), b_scale_strides=(up(K, 128), 1)))
         names.add(h.info.name.decode())
     assert names == {"narrow_64x64", "stream_16x32_w4", "stream_16x16_w8", "stream_32x32_w4", "stream_64x32_w4",
-                     "tile_64x128_w2x2", "tile_128x128_w2x2", "pingpong_256x256"}
+                     "tile_64x128_w2x2", "tile_64x128_w2x2x2", "tile_128x128_w2x2", "tile_128x128_w2x2x2",
+                     "pingpong_256x256"}
