@@ -39,30 +39,46 @@ template <> struct XType<DT_F16> {
   __device__ static float up(u16 v) { return f16_to_f32(v); }
 };
 
-// The source row of result row r, or -1 for a row of zeros.
-__device__ __forceinline__ int64_t source_row(const QParams& p, int64_t r) {
-  if (!p.index) return r;
-  const int i = p.index[r];
-  if (i < 0) return -1;
-  const int64_t s = p.index_div == 1 ? i : i / p.index_div;
-  return s < p.x_rows ? s : -1;
+// The source rows of result rows r .. r + N - 1, -1 for a row of zeros.  All indices are loaded
+// before one is used.
+template <int N> __device__ __forceinline__ void source_rows(const QParams& p, int64_t r, int64_t (&s)[N]) {
+  if (!p.index) {
+    static_for<N>([&](auto i) { s[i] = r + i < p.rows ? r + i : -1; });
+    return;
+  }
+  int at[N];
+  static_for<N>([&](auto i) { at[i] = p.index[min(r + i, p.rows - 1)]; });
+  static_for<N>([&](auto i) {
+    const bool ok = r + i < p.rows && at[i] >= 0;
+    const int64_t q = p.index_div == 1 ? at[i] : (int)((u32)at[i] / (u32)p.index_div);
+    s[i] = ok && q < p.x_rows ? q : -1;
+  });
 }
 
+// Loads have clamped addresses in place of conditions, and what they fetch in vain is dropped
+// afterwards: loads under conditions of their own wait for each other (64 single ones of a patch of
+// 8 x 8 at odd columns took 12 us).
+//
 // Columns c .. c + 7 of source row s as fp32; zero past the row and for s < 0.
 template <int XT>
 __device__ __forceinline__ void load8(const QParams& p, int64_t s, int64_t c, float (&v)[8]) {
   typedef typename XType<XT>::T T;
-  const T* src = (const T*)p.x + s * p.ldx + c;
-  if (s >= 0 && p.x_vec && c + 8 <= p.cols) {
+  static_for<8>([&](auto i) { v[i] = 0.f; });
+  if (p.x_rows == 0) return;        // there is nothing to clamp to
+  const T* src = (const T*)p.x + max(s, (int64_t)0) * p.ldx;
+  if (p.x_vec && c + 8 <= p.cols) {
     constexpr int PER = 16 / (int)sizeof(T);
     static_for<8 / PER>([&](auto h) {
-      const u32x4 w = reinterpret_cast<const u32x4*>(src)[(int)h];
+      const u32x4 w = reinterpret_cast<const u32x4*>(src + c)[(int)h];
       const T* e = reinterpret_cast<const T*>(&w);
       static_for<PER>([&](auto i) { v[h * PER + i] = XType<XT>::up(e[(int)i]); });
     });
   } else {
-    static_for<8>([&](auto i) { v[i] = s >= 0 && c + i < p.cols ? XType<XT>::up(src[(int)i]) : 0.f; });
+    T e[8];
+    static_for<8>([&](auto i) { e[i] = src[min(c + i, p.cols - 1)]; });
+    static_for<8>([&](auto i) { v[i] = c + i < p.cols ? XType<XT>::up(e[i]) : 0.f; });
   }
+  static_for<8>([&](auto i) { v[i] = s < 0 ? 0.f : v[i]; });
 }
 
 // |x| as an integer: ordered as the magnitudes are, with infinity and then NaN above all.
@@ -77,12 +93,11 @@ __device__ __forceinline__ u32 row_max(u32 v) {
 }
 
 struct Scale {
-  float scale, inverse;
-  bool bad;
+  float scale, inverse;   // both NaN for a block with an infinity or a NaN
 };
 __device__ __forceinline__ Scale scale_of(u32 top, int pow2) {
   Scale s;
-  s.bad = top >= 0x7f800000u;
+  const bool bad = top >= 0x7f800000u;
   if (pow2) {
     // top = 1.f * 2^e: the least power of two s with top / s <= 448 = 1.75 * 2^8 is 2^(e - 8), one
     // more when the fraction is above 1.75
@@ -91,20 +106,20 @@ __device__ __forceinline__ Scale scale_of(u32 top, int pow2) {
     s.scale = __builtin_bit_cast(float, (u32)(c + 127) << 23);
     s.inverse = __builtin_bit_cast(float, (u32)(127 - c) << 23);
   } else {
-    const float t = fmaxf(__builtin_bit_cast(float, s.bad ? 0u : top), 448.f * 0x1p-126f);
+    const float t = fmaxf(__builtin_bit_cast(float, bad ? 0u : top), 448.f * 0x1p-126f);
     s.scale = t / 448.f;
     s.inverse = 448.f / t;
   }
-  if (s.bad) s.scale = __builtin_nanf("");
+  if (bad) s.scale = s.inverse = __builtin_nanf("");
   return s;
 }
 
 // Four e4m3 codes; the products are rounded to fp32, then to nearest even in the conversion.
-__device__ __forceinline__ u32 codes4(float a, float b, float c, float d, const Scale& s) {
-  if (s.bad) return 0x7f7f7f7fu;
-  auto clip = [&](float v) { return __builtin_amdgcn_fmed3f(v * s.inverse, -448.f, 448.f); };
+__device__ __forceinline__ u32 codes4(float a, float b, float c, float d, float inverse) {
+  auto clip = [&](float v) { return __builtin_amdgcn_fmed3f(v * inverse, -448.f, 448.f); };
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(clip(a), clip(b), 0, false);
-  return (u32)__builtin_amdgcn_cvt_pk_fp8_f32(clip(c), clip(d), w, true);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(clip(c), clip(d), w, true);
+  return inverse == inverse ? (u32)w : 0x7f7f7f7fu;
 }
 
 // 8 codes at row r, columns c .. c + 7: those below `cols` data, zeros up to q_cols.
@@ -114,12 +129,15 @@ __device__ __forceinline__ void store8(const QParams& p, int64_t r, int64_t c, u
   if (p.q_vec && c + 8 <= p.q_cols) {
     *reinterpret_cast<uint64_t*>(d) = w;
   } else {
-    static_for<8>([&](auto i) { if (c + i < p.q_cols) d[(int)i] = (u8)(w >> (8 * i)); });
+    const int n = (int)min((int64_t)8, p.q_cols - c);
+    uint64_t left = w;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i, left >>= 8) d[i] = (u8)left;
   }
 }
 // Codes past the data are zero even in a block whose scale is NaN.
-__device__ __forceinline__ u32 keep(u32 w, int64_t left) {
-  return left >= 4 ? w : left <= 0 ? 0u : w & (0xffffffffu >> (8 * (4 - (int)left)));
+__device__ __forceinline__ u32 keep(u32 w, int left) {
+  return left >= 4 ? w : left <= 0 ? 0u : w & (0xffffffffu >> (8 * (4 - left)));
 }
 
 // Scales for each row and 128 columns, row-major: a wave takes 512 columns of a row, a lane 8
@@ -131,12 +149,15 @@ __global__ __launch_bounds__(256) void quant_rows(const QParams p, int64_t units
   if (u >= units) return;
   const int64_t r = u / segs, c = (u - r * segs) * 512 + lane * 8;
   float v[8];
-  load8<XT>(p, source_row(p, r), c, v);
+  int64_t s1[1];
+  source_rows<1>(p, r, s1);
+  load8<XT>(p, s1[0], c, v);
   u32 m = 0;
   static_for<8>([&](auto i) { m = max(m, mag(v[i])); });
   const Scale s = scale_of(row_max(m), p.pow2);
-  store8(p, r, c, keep(codes4(v[0], v[1], v[2], v[3], s), p.cols - c),
-         keep(codes4(v[4], v[5], v[6], v[7], s), p.cols - c - 4));
+  const int left = (int)(p.cols - c);
+  store8(p, r, c, keep(codes4(v[0], v[1], v[2], v[3], s.inverse), left),
+         keep(codes4(v[4], v[5], v[6], v[7], s.inverse), left - 4));
   if ((lane & 15) == 0 && c < p.cols) p.scale[r * p.scale_r + c / 128 * p.scale_c] = s.scale;
 }
 
@@ -145,14 +166,23 @@ __global__ __launch_bounds__(256) void quant_rows(const QParams p, int64_t units
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 template <int XT> struct Patch {
   u32x4 w[8];
-  __device__ __forceinline__ void load(const QParams& p, int i, int64_t s, int64_t c) {
-    const u16* src = (const u16*)p.x + s * p.ldx + c;
-    w[i] = u32x4{0, 0, 0, 0};
-    if (s >= 0 && p.x_vec && c + 8 <= p.cols) {
-      w[i] = *reinterpret_cast<const u32x4*>(src);
-    } else if (s >= 0) {
-      static_for<8>([&](auto e) { if (c + e < p.cols) w[i][(int)e / 2] |= (u32)src[(int)e] << (16 * (e % 2)); });
+  __device__ __forceinline__ void load(const QParams& p, const int64_t (&s)[8], int64_t c) {
+    static_for<8>([&](auto i) { w[i] = u32x4{0, 0, 0, 0}; });
+    if (p.x_rows == 0) return;
+    const u16* x = (const u16*)p.x;
+    if (p.x_vec && c + 8 <= p.cols) {
+      static_for<8>([&](auto i) { w[i] = *reinterpret_cast<const u32x4*>(x + max(s[i], (int64_t)0) * p.ldx + c); });
+    } else {
+      static_for<8>([&](auto i) {
+        const u16* src = x + max(s[i], (int64_t)0) * p.ldx;
+        u32 e[8];
+        static_for<8>([&](auto j) { e[j] = src[min(c + j, p.cols - 1)]; });
+        static_for<4>([&](auto d) {
+          w[i][(int)d] = (c + 2 * d < p.cols ? e[2 * d] : 0u) | (c + 2 * d + 1 < p.cols ? e[2 * d + 1] << 16 : 0u);
+        });
+      });
     }
+    static_for<8>([&](auto i) { w[i] = s[i] < 0 ? u32x4{0, 0, 0, 0} : w[i]; });
   }
   template <int I, int J> __device__ __forceinline__ float at() const {
     if constexpr (XT == DT_BF16) return __builtin_bit_cast(float, J % 2 ? w[I][J / 2] & 0xffff0000u : w[I][J / 2] << 16);
@@ -181,7 +211,9 @@ template <int XT> struct Patch {
 };
 template <> struct Patch<DT_F32> {
   float v[8][8];
-  __device__ __forceinline__ void load(const QParams& p, int i, int64_t s, int64_t c) { load8<DT_F32>(p, s, c, v[i]); }
+  __device__ __forceinline__ void load(const QParams& p, const int64_t (&s)[8], int64_t c) {
+    static_for<8>([&](auto i) { load8<DT_F32>(p, s[i], c, v[i]); });
+  }
   template <int I, int J> __device__ __forceinline__ float at() const { return v[I][J]; }
   __device__ __forceinline__ u32 row_top(int i) const {
     u32 m = 0;
@@ -198,63 +230,78 @@ template <> struct Patch<DT_F32> {
 
 // A 128 x 128 tile: row-major and transposed codes from one read, with scales by row and by
 // column, or one scale for the tile.  Thread (ty, lx) holds rows 8 ty .. + 7 of columns 8 lx .. + 7;
-// the transposed codes go through LDS (chunk ^ column / 8, so that the 16 lanes of a write fall on
-// different banks) and leave as 16-byte chunks.  8192 x 8192 bf16 both ways: 71 us, 3.9 TB/s (a copy
-// reaches 4.7); with the values unpacked to fp32 (167 registers in place of 68) 94 us.
+// thread i makes the scale of column i or row i - 128 from the maxima in LDS, once, which keeps the
+// code short: a small matrix pays for fetching it.  The transposed codes go through LDS (chunk ^
+// column / 8, so that the 16 lanes of a write fall on different banks) and leave as 16-byte chunks.
+// 8192 x 8192 bf16 both ways: 60 us, 4.6 TB/s (a copy reaches 4.7); with each thread making the
+// scales of all its rows and columns 73 us, a matrix of 21 x 3323 19 us in place of 12.
 template <int XT>
 __global__ __launch_bounds__(256) void quant_tiles(const QParams p, int tiles_c) {
-  __shared__ u32 colmax[128];
+  __shared__ u32 tops[256];       // of the columns, then the rows; [0] of the tile
+  __shared__ alignas(16) float inverse[256];
   __shared__ uint64_t turned[128 * 16];
   const int tid = threadIdx.x, lx = tid & 15, ty = tid >> 4;
   const int64_t rb = blockIdx.x / tiles_c, cb = blockIdx.x % tiles_c;
   const int64_t r0 = rb * 128 + ty * 8, c0 = cb * 128 + lx * 8;
-  if (tid < 128) colmax[tid] = 0;
+  tops[tid] = 0;
   Patch<XT> v;
-  static_for<8>([&](auto i) {
-    const int64_t r = r0 + i;
-    v.load(p, i, r < p.rows ? source_row(p, r) : -1, c0);
-  });
+  int64_t from[8];
+  source_rows<8>(p, r0, from);
+  v.load(p, from, c0);
   __syncthreads();
-  Scale tile;
+  // maxima: the same whatever the order
   if (p.block) {
     u32 m = 0;
     static_for<8>([&](auto i) { m = max(m, v.row_top(i)); });
     m = row_max(m);
-    if (lx == 0) atomicMax(&colmax[0], m);  // a maximum: the same whatever the order
-    __syncthreads();
-    tile = scale_of(colmax[0], p.pow2);
-    if (tid == 0) p.scale[rb * p.scale_r + cb * p.scale_c] = tile.scale;
-  } else if (p.qt) {
-    u32 top[8];
-    v.col_top(top);
-    static_for<8>([&](auto j) {
-      u32 m = top[j];
-      m = max(m, (u32)__shfl_xor((int)m, 16, 64));
-      m = max(m, (u32)__shfl_xor((int)m, 32, 64));
-      if ((tid & 48) == 0) atomicMax(&colmax[lx * 8 + j], m);
-    });
-    __syncthreads();
+    if (lx == 0) atomicMax(&tops[0], m);
+  } else {
+    if (p.qt) {
+      u32 top[8];
+      v.col_top(top);
+      static_for<8>([&](auto j) {
+        u32 m = top[j];
+        m = max(m, (u32)__shfl_xor((int)m, 16, 64));
+        m = max(m, (u32)__shfl_xor((int)m, 32, 64));
+        if ((tid & 48) == 0) atomicMax(&tops[lx * 8 + j], m);
+      });
+    }
+    if (p.q) {
+      static_for<8>([&](auto i) {
+        const u32 m = row_max(v.row_top(i));
+        if (lx == 0) tops[128 + ty * 8 + i] = m;
+      });
+    }
   }
+  __syncthreads();
+  const Scale s = scale_of(tops[p.block ? 0 : tid], p.pow2);
+  inverse[tid] = s.inverse;
+  if (p.block) {
+    if (tid == 0) p.scale[rb * p.scale_r + cb * p.scale_c] = s.scale;
+  } else if (tid < 128) {
+    const int64_t c = cb * 128 + tid;
+    if (p.qt && c < p.cols) p.scale_t[c * p.scale_t_c + rb * p.scale_t_r] = s.scale;
+  } else {
+    const int64_t r = rb * 128 + tid - 128;
+    if (p.q && r < p.rows) p.scale[r * p.scale_r + cb * p.scale_c] = s.scale;
+  }
+  __syncthreads();
+  const int rows = (int)(p.rows - r0), cols = (int)(p.cols - c0);   // of the patch that are data
   if (p.qt) {
     static_for<8>([&](auto j) {
       const int col = lx * 8 + j;
-      const Scale s = p.block ? tile : scale_of(colmax[col], p.pow2);
-      const u32 lo = keep(codes4(v.template at<0, j>(), v.template at<1, j>(), v.template at<2, j>(), v.template at<3, j>(), s), p.rows - r0);
-      const u32 hi = keep(codes4(v.template at<4, j>(), v.template at<5, j>(), v.template at<6, j>(), v.template at<7, j>(), s), p.rows - r0 - 4);
+      const float f = inverse[col];
+      const u32 lo = keep(codes4(v.template at<0, j>(), v.template at<1, j>(), v.template at<2, j>(), v.template at<3, j>(), f), rows);
+      const u32 hi = keep(codes4(v.template at<4, j>(), v.template at<5, j>(), v.template at<6, j>(), v.template at<7, j>(), f), rows - 4);
       turned[col * 16 + (((ty >> 1) ^ (lx & 7)) << 1 | (ty & 1))] = (uint64_t)hi << 32 | lo;
-      if (!p.block && ty == 0 && c0 + j < p.cols)
-        p.scale_t[(c0 + j) * p.scale_t_c + rb * p.scale_t_r] = s.scale;
     });
   }
   if (p.q) {
     static_for<8>([&](auto i) {
-      const int64_t r = r0 + i;
-      const Scale s = p.block ? tile : scale_of(row_max(v.row_top(i)), p.pow2);
-      if (r < p.rows) {
-        store8(p, r, c0, keep(codes4(v.template at<i, 0>(), v.template at<i, 1>(), v.template at<i, 2>(), v.template at<i, 3>(), s), p.cols - c0),
-               keep(codes4(v.template at<i, 4>(), v.template at<i, 5>(), v.template at<i, 6>(), v.template at<i, 7>(), s), p.cols - c0 - 4));
-        if (!p.block && lx == 0) p.scale[r * p.scale_r + cb * p.scale_c] = s.scale;
-      }
+      const float f = inverse[128 + ty * 8 + i];
+      if (i < rows)
+        store8(p, r0 + i, c0, keep(codes4(v.template at<i, 0>(), v.template at<i, 1>(), v.template at<i, 2>(), v.template at<i, 3>(), f), cols),
+               keep(codes4(v.template at<i, 4>(), v.template at<i, 5>(), v.template at<i, 6>(), v.template at<i, 7>(), f), cols - 4));
     });
   }
   if (!p.qt) return;
@@ -331,7 +378,7 @@ extern "C" int quant_blocks(const quant_args* a, void* stream) {
   p.rows = a->rows;
   p.cols = a->cols;
   p.ldx = a->ldx;
-  p.x_rows = a->x_rows;
+  p.x_rows = a->row_index ? a->x_rows : a->rows;
   p.ldq = a->ldq;
   p.ldqt = a->ldqt;
   p.q_cols = !a->q ? 0 : a->pad ? std::min(a->ldq, (a->cols + 15) / 16 * 16) : a->cols;

@@ -222,3 +222,17 @@ def test_captured_and_replayed():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(q, e[0]) and torch.equal(qt, e[1]) and torch.equal(s, e[2]) and torch.equal(st, e[3])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_of_an_empty_matrix(dtype):
+    """Every index points outside a matrix without rows: zeros, with the least scale."""
+    x = torch.empty(0, 200, dtype=dtype, device="cuda")
+    at = torch.tensor([-1, 0, 5, 2 ** 31 - 1, -2 ** 31] * 30, dtype=torch.int32, device="cuda")
+    q = torch.full((150, 200), 9, dtype=torch.uint8, device="cuda")
+    qt = torch.full((200, 150), 9, dtype=torch.uint8, device="cuda")
+    s, st = torch.full((150, 2), -1.0, device="cuda"), torch.full((200, 2), -1.0, device="cuda")
+    for both in (False, True):
+        S.quantize(x, q, s, qt if both else None, st if both else None, row_index=at)
+        assert (q == 0).all() and (s == 2.0 ** -126).all()
+    assert (qt == 0).all() and (st == 2.0 ** -126).all()
