@@ -5,9 +5,10 @@ device addresses); every buffer is the caller's.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 from . import htgemm
-from .htgemm import ACTS, DTYPES, GEMM_ERR_INVALID_ARG, GemmError, _addr, _check
+from .htgemm import ACTS, DTYPES, GEMM_ERR_INVALID_ARG, GemmError, _check
 from .htgemm import _stream as _stream_of
 
 FORMS = {"single": 0, "batch": 1, "rows": 2, "k": 3}
@@ -81,7 +82,7 @@ def lib():
         for name, args in {
                 "gemm_scaled_create": [P(gemm_scaled_desc), P(_vp)],
                 "gemm_scaled_workspace_size": [_vp, P(ctypes.c_size_t)],
-                "gemm_scaled_run": [_vp, P(gemm_scaled_args), _vp],
+                "gemm_scaled_run": [_vp, _vp, _vp],
                 "gemm_scaled_get_info": [_vp, P(gemm_scaled_info)],
                 "gemm_scaled_destroy": [_vp],
                 "quant_blocks": [P(quant_args), _vp]}.items():
@@ -111,8 +112,66 @@ def make_desc(M, N, K, out="bf16", *, lda, ldb, ldd, ldc=0, b_block=128, a_scale
     return d
 
 
+_KINDS = {}
+
+
+def _kinds(d_type):
+    """The types of a description's codes, scales, outputs (C and bias among them) and offsets."""
+    if not _KINDS:
+        import torch
+        codes, f32, i32 = (torch.float8_e4m3fn, torch.uint8, torch.int8), (torch.float32,), (torch.int32,)
+        _KINDS.update({DTYPES["bf16"]: (codes, f32, (torch.bfloat16,), i32), DTYPES["f32"]: (codes, f32, f32, i32)})
+    return _KINDS[d_type]
+
+
+def _extents(d):
+    """How many values from the first on A, a_scale, B, b_scale, C, D, bias, row_scale and offsets have
+    to hold for a product of description d."""
+    M, N, K, L = d.M, d.N, d.K, d.batch if d.form != FORMS["single"] else 1
+    if M == 0 or N == 0:
+        return (0,) * 9
+    form = d.form
+    a_many = L - 1 if form == FORMS["batch"] else 0
+    b_many = L - 1 if form in (FORMS["batch"], FORMS["rows"]) else 0
+    d_many = L - 1 if form in (FORMS["batch"], FORMS["k"]) else 0
+    kb, nb = -(-K // 128), -(-N // d.b_block)
+    a = a_many * d.a_stride_l + (M - 1) * d.lda + K if K else 0
+    b = b_many * d.b_stride_l + (N - 1) * d.ldb + K if K else 0
+    a_scale = a_many * d.a_scale_l + (M - 1) * d.a_scale_m + (kb - 1) * d.a_scale_k + 1 if K else 0
+    b_scale = b_many * d.b_scale_l + (nb - 1) * d.b_scale_n + (kb - 1) * d.b_scale_k + 1 if K else 0
+    c = d_many * d.c_stride_l + (M - 1) * d.ldc + N if d.has_c else 0
+    return (a, a_scale, b, b_scale, c, d_many * d.d_stride_l + (M - 1) * d.ldd + N, N if d.has_bias else 0,
+            M if d.has_row_scale else 0, L + 1 if form in (FORMS["rows"], FORMS["k"]) else 0)
+
+
+def _bytes(t):
+    """Bytes of a tensor's memory from its first value on, whatever its shape."""
+    size = t.element_size()
+    return t.untyped_storage().nbytes() - t.storage_offset() * size
+
+
+def _address(t, kinds, n, dev):
+    """Address of a tensor on device dev whose type is one of `kinds` and whose memory has n values
+    from the first on; an address (or None) as it is."""
+    if t is None or t.__class__ is int:
+        return t or 0
+    if t.get_device() != dev or t.dtype not in kinds or not (
+            (t.numel() >= n and t.is_contiguous()) or _bytes(t) >= n * t.element_size()):
+        raise GemmError(GEMM_ERR_INVALID_ARG, "gemm_scaled_run")
+    return t.data_ptr()
+
+
+_ARGS = struct.Struct("@9P2fP")   # gemm_scaled_args, filled by one call
+assert _ARGS.size == ctypes.sizeof(gemm_scaled_args)
+
+
 class ScaledGemm:
-    """RAII wrapper: a handle for one block-scaled product description."""
+    """RAII wrapper: a handle for one block-scaled product description.
+
+    run() raises GemmError for tensors on another device than the current one, of another type than
+    the description's (codes: uint8, int8 or float8_e4m3fn), or whose memory ends before the
+    product's does, and for a workspace of fewer than workspace_bytes.  Device addresses are taken
+    as they are.  C is looked at only when beta is not 0."""
 
     def __init__(self, desc: gemm_scaled_desc):
         self.handle = None
@@ -120,6 +179,9 @@ class ScaledGemm:
         h = _vp()
         _check(lib().gemm_scaled_create(ctypes.byref(desc), ctypes.byref(h)), "gemm_scaled_create")
         self.handle = h.value
+        self._kinds = _kinds(desc.d_type)
+        self._extents = _extents(desc)
+        self._room = self.workspace_bytes
 
     @property
     def info(self) -> gemm_scaled_info:
@@ -135,15 +197,39 @@ class ScaledGemm:
 
     def run(self, A, a_scale, B, b_scale, D, C=None, bias=None, row_scale=None, offsets=None, alpha=1.0,
             beta=0.0, workspace=None, stream=None):
-        a = gemm_scaled_args(_addr(A), _addr(a_scale), _addr(B), _addr(b_scale), None if C is None else _addr(C),
-                             _addr(D), None if bias is None else _addr(bias),
-                             None if row_scale is None else _addr(row_scale),
-                             None if offsets is None else _addr(offsets), alpha, beta,
-                             None if workspace is None else _addr(workspace))
         dev, stream = _here(stream)
-        if _elsewhere(dev, A, a_scale, B, b_scale, C, D, bias, row_scale, offsets, workspace):
-            raise GemmError(GEMM_ERR_INVALID_ARG, "gemm_scaled_run")
-        rc = _lib.gemm_scaled_run(self.handle, ctypes.byref(a), stream)
+        codes, f32, out, i32 = self._kinds
+        nA, nSA, nB, nSB, nC, nD, n_bias, n_rows, n_offsets = self._extents
+        try:
+            # the usual tensors, whole and of the right type, in one expression: _address for each
+            # takes a call a microsecond more
+            usual = (A.get_device() == dev and A.dtype in codes and A.numel() >= nA and A.is_contiguous() and
+                     B.get_device() == dev and B.dtype in codes and B.numel() >= nB and B.is_contiguous() and
+                     D.get_device() == dev and D.dtype in out and D.numel() >= nD and D.is_contiguous() and
+                     a_scale.get_device() == dev and a_scale.dtype in f32 and a_scale.numel() >= nSA and
+                     a_scale.is_contiguous() and
+                     b_scale.get_device() == dev and b_scale.dtype in f32 and b_scale.numel() >= nSB and
+                     b_scale.is_contiguous())
+        except AttributeError:      # an address or None
+            usual = False
+        if usual:
+            A, a_scale, B, b_scale, D = A.data_ptr(), a_scale.data_ptr(), B.data_ptr(), b_scale.data_ptr(), D.data_ptr()
+        else:
+            A, a_scale = _address(A, codes, nA, dev), _address(a_scale, f32, nSA, dev)
+            B, b_scale = _address(B, codes, nB, dev), _address(b_scale, f32, nSB, dev)
+            D = _address(D, out, nD, dev)
+        C = 0 if C is None or not beta else _address(C, out, nC, dev)
+        bias = 0 if bias is None else _address(bias, out, n_bias, dev)
+        row_scale = 0 if row_scale is None else _address(row_scale, f32, n_rows, dev)
+        offsets = 0 if offsets is None else _address(offsets, i32, n_offsets, dev)
+        if workspace is None:
+            workspace = 0
+        elif workspace.__class__ is not int:
+            if workspace.get_device() != dev or (self._room and _bytes(workspace) < self._room):
+                raise GemmError(GEMM_ERR_INVALID_ARG, "gemm_scaled_run")
+            workspace = workspace.data_ptr()
+        rc = _lib.gemm_scaled_run(self.handle, _ARGS.pack(A, a_scale, B, b_scale, C, D, bias, row_scale, offsets, alpha, beta,
+                                                          workspace), stream)
         if rc:
             raise GemmError(rc, "gemm_scaled_run")
 
