@@ -140,12 +140,21 @@ __device__ __forceinline__ u32 keep(u32 w, int left) {
   return left >= 4 ? w : left <= 0 ? 0u : w & (0xffffffffu >> (8 * (4 - left)));
 }
 
+// A dimension of a launch has fewer than 2^32 threads, and one with more runs as what is left modulo
+// 2^32, without an error: the workgroups are dealt over two dimensions.
+constexpr int64_t kMostX = int64_t(1) << 22;
+dim3 grid_of(int64_t blocks) {
+  const int64_t x = std::min(blocks, kMostX);
+  return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
+}
+__device__ __forceinline__ u32 block_id() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Scales for each row and 128 columns, row-major: a wave takes 512 columns of a row, a lane 8
 // neighbouring ones, the 16 lanes of a DPP row one block.  One row of 8192: 2.7 us, a launch.
 template <int XT>
 __global__ __launch_bounds__(256) void quant_rows(const QParams p, int64_t units, int segs) {
   const int lane = threadIdx.x & 63;
-  const int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t u = (int64_t)block_id() * 4 + (threadIdx.x >> 6);
   if (u >= units) return;
   const int64_t r = u / segs, c = (u - r * segs) * 512 + lane * 8;
   float v[8];
@@ -236,12 +245,14 @@ template <> struct Patch<DT_F32> {
 // 8192 x 8192 bf16 both ways: 60 us, 4.6 TB/s (a copy reaches 4.7); with each thread making the
 // scales of all its rows and columns 73 us, a matrix of 21 x 3323 19 us in place of 12.
 template <int XT>
-__global__ __launch_bounds__(256) void quant_tiles(const QParams p, int tiles_c) {
+__global__ __launch_bounds__(256) void quant_tiles(const QParams p, int tiles_c, u32 tiles) {
   __shared__ u32 tops[256];       // of the columns, then the rows; [0] of the tile
   __shared__ alignas(16) float inverse[256];
   __shared__ uint64_t turned[128 * 16];
   const int tid = threadIdx.x, lx = tid & 15, ty = tid >> 4;
-  const int64_t rb = blockIdx.x / tiles_c, cb = blockIdx.x % tiles_c;
+  const u32 tile = block_id();
+  if (tile >= tiles) return;
+  const int64_t rb = tile / (u32)tiles_c, cb = tile % (u32)tiles_c;
   const int64_t r0 = rb * 128 + ty * 8, c0 = cb * 128 + lx * 8;
   tops[tid] = 0;
   Patch<XT> v;
@@ -328,11 +339,11 @@ template <int XT> hipError_t launch(const QParams& p, hipStream_t s, bool* too_l
   if (!p.block && !p.qt) {
     const int64_t segs = (p.q_cols + 511) / 512, units = p.rows * segs, blocks = (units + 3) / 4;
     if (blocks > INT32_MAX) { *too_large = true; return hipSuccess; }
-    hipLaunchKernelGGL(quant_rows<XT>, dim3((unsigned)blocks), dim3(256), 0, s, p, units, (int)segs);
+    hipLaunchKernelGGL(quant_rows<XT>, grid_of(blocks), dim3(256), 0, s, p, units, (int)segs);
   } else {
     const int64_t tc = (p.cols + 127) / 128, blocks = (p.rows + 127) / 128 * tc;
     if (blocks > INT32_MAX) { *too_large = true; return hipSuccess; }
-    hipLaunchKernelGGL(quant_tiles<XT>, dim3((unsigned)blocks), dim3(256), 0, s, p, (int)tc);
+    hipLaunchKernelGGL(quant_tiles<XT>, grid_of(blocks), dim3(256), 0, s, p, (int)tc, (u32)blocks);
   }
   return hipGetLastError();
 }
