@@ -103,6 +103,11 @@ int64_t row_tiles(const gemm_scaled_s& h, int bm) {
   return h.d.form == GEMM_SCALED_ROWS ? std::min(h.d.M, h.d.M / bm + h.batch) : t;
 }
 
+// Workgroups of a launch along x, and whether a launch can have them: a dimension of one has fewer
+// than 2^32 threads, and the runtime runs one with more as what is left modulo 2^32, without an error.
+int64_t grid_x(const gemm_scaled_s& h, const Variant& v) { return row_tiles(h, v.bm) * up(h.d.N, v.bn); }
+bool fits(const gemm_scaled_s& h, const Variant& v) { return grid_x(h, v) * v.waves * 64 <= int64_t(UINT32_MAX); }
+
 // Expected row tiles of a launch, for groups of rows from a routing that spreads M rows over the
 // groups: the groups that get any, and what a group's last tile leaves empty.
 double expected_row_tiles(const gemm_scaled_s& h, int bm) {
@@ -158,7 +163,7 @@ void choose(gemm_scaled_s* h) {
   double best = 0.0;
   for (int i = V_NARROW + 1; i < V_COUNT; ++i) {
     const Variant& v = kVariants[i];
-    if (!v.launch[bb][f32] || (i == V_PP && d.a_scale_m != 1)) continue;
+    if (!v.launch[bb][f32] || (i == V_PP && d.a_scale_m != 1) || !fits(*h, v)) continue;
     for (int s = 1; s <= 16; s *= 2) {
       const bool forced = d.split_k > 0 || d.form != GEMM_SCALED_SINGLE;
       if (forced && s > 1) break;
@@ -212,6 +217,7 @@ int gemm_scaled_create(const gemm_scaled_desc* desc, gemm_scaled_t* out) {
           (!(batch || rows) || d.b_stride_l % 16 == 0) && 256 * d.lda + d.K < (int64_t(1) << 31) &&
           256 * d.ldb + d.K < (int64_t(1) << 31);
   choose(&h);
+  if (!fits(h, kVariants[h.variant])) return GEMM_ERR_INVALID_ARG;
   gemm_scaled_s* p = new (std::nothrow) gemm_scaled_s(h);
   if (!p) return GEMM_ERR_INVALID_ARG;
   p->magic = kLive;
@@ -236,7 +242,7 @@ int gemm_scaled_get_info(gemm_scaled_t h, gemm_scaled_info* info) {
   info->waves = v.waves;
   info->lds_bytes = v.lds;
   info->split_k = h->split;
-  info->grid = row_tiles(*h, v.bm) * up(h->d.N, v.bn) * h->split * (h->d.form == GEMM_SCALED_ROWS ? 1 : h->batch);
+  info->grid = grid_x(*h, v) * h->split * (h->d.form == GEMM_SCALED_ROWS ? 1 : h->batch);
   std::strncpy(info->name, v.name, sizeof(info->name) - 1);
   return GEMM_OK;
 }
@@ -300,8 +306,8 @@ int gemm_scaled_run(gemm_scaled_t h, const gemm_scaled_args* a, void* stream) {
   p.tiles_n = (int)up(d.N, v.bn);
   p.split_k = split;
   p.blocks_per_split = (int)h->per;
-  const int64_t grid = row_tiles(*h, v.bm) * p.tiles_n;
-  if (grid > INT32_MAX) return GEMM_ERR_INVALID_ARG;
+  if (!fits(*h, v)) return GEMM_ERR_INVALID_ARG;     // of a handle made for another alignment
+  const int64_t grid = grid_x(*h, v);
   const unsigned gz = d.form == GEMM_SCALED_ROWS ? 1 : (unsigned)h->batch;
   hipStream_t s = (hipStream_t)stream;
   const int bb = d.b_block == 1, f32 = d.d_type == GEMM_F32;

@@ -57,7 +57,7 @@ typedef struct gemm_scaled_desc {
 typedef struct gemm_scaled_s* gemm_scaled_t;
 
 /* Validate `desc` and choose a kernel.  Host only.  Errors: GEMM_ERR_INVALID_ARG (a negative or
- * too large size, an unknown enum, a split of a batch or of groups, batch < 1 with a form that
+ * too large size -- also of a launch, which has fewer than 2^32 threads --, an unknown enum, a split of a batch or of groups, batch < 1 with a form that
  * needs it, d_stride_l == 0 where products would overwrite each other), GEMM_ERR_DTYPE_COMBO,
  * GEMM_ERR_LAYOUT (a leading dimension below its row, a negative stride), GEMM_ERR_ARCH,
  * GEMM_ERR_HIP.
@@ -100,8 +100,8 @@ typedef struct gemm_scaled_args {
  * behind the last are not written.  With GEMM_SCALED_K every offset is also rounded down to a
  * multiple of 128, except one that equals K, because a block of k has one scale.
  *
- * Errors: GEMM_ERR_BAD_HANDLE, GEMM_ERR_INVALID_ARG (a missing or a superfluous pointer),
- * GEMM_ERR_MISALIGNED, GEMM_ERR_LAUNCH.  An error launches nothing. */
+ * Errors: GEMM_ERR_BAD_HANDLE, GEMM_ERR_INVALID_ARG (a missing or a superfluous pointer, or more than
+ * 2^32 threads of the kernel that these pointers' alignment needs), GEMM_ERR_MISALIGNED, GEMM_ERR_LAUNCH.  An error launches nothing. */
 int gemm_scaled_run(gemm_scaled_t h, const gemm_scaled_args* args, void* stream);
 
 /* Free a handle.  NULL is accepted. */
