@@ -51,10 +51,12 @@ HEADERS = [os.path.join(CSRC, "kernels.h"), os.path.join(CSRC, "pingpong.h"), os
            os.path.join(CSRC, "atom_maps.h"),
            os.path.join(ROOT, "include", "htgemm.h"), os.path.join(ROOT, "include", "htlayout.h")]
 # headers that only some sources read, besides those
+ARCH_H = os.path.join(CSRC, "arch.h")
 OWN_HEADERS = {
-    "scaled.hip": [os.path.join(CSRC, "scaled.h"), os.path.join(ROOT, "include", "htscaled.h")],
-    "quant.hip": [os.path.join(ROOT, "include", "htscaled.h")],
-    "route.hip": [os.path.join(ROOT, "include", "htroute.h")],
+    "api.cpp": [ARCH_H],
+    "scaled.hip": [ARCH_H, os.path.join(CSRC, "scaled.h"), os.path.join(ROOT, "include", "htscaled.h")],
+    "quant.hip": [ARCH_H, os.path.join(ROOT, "include", "htscaled.h")],
+    "route.hip": [ARCH_H, os.path.join(ROOT, "include", "htroute.h")],
 }
 
 

@@ -22,6 +22,7 @@
 
 #include "../../include/htgemm.h"
 #include "../../include/htlayout.h"
+#include "arch.h"
 #include "atom_maps.h"
 #include "gemm_internal.h"
 

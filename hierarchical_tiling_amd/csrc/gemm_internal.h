@@ -160,9 +160,6 @@ hipError_t launch_repack_pair(const void* a_src, void* a_dst, int64_t a_rows, in
 hipError_t launch_group_scan(const int32_t* offsets, int G, int64_t M, int bm, int tiles_n,
                              int32_t* lo, int64_t* base, hipStream_t s);
 
-// Whether the current device is a gfx950, as a status code; remembered for each device.
-int arch_status();
-
 // Output type of a given operand type (htgemm.h type table).
 constexpr int out_dtype(int dt) { return dt == DT_F8 ? DT_BF16 : dt; }
 constexpr int dtype_size(int dt) { return dt == DT_F32 ? 4 : (dt == DT_F8 ? 1 : 2); }

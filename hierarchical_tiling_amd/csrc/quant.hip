@@ -6,6 +6,7 @@
 #include <algorithm>
 
 #include "../../include/htscaled.h"
+#include "arch.h"
 #include "kernels.h"
 
 namespace htk {

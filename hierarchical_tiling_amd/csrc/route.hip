@@ -3,6 +3,7 @@
 #include <algorithm>
 
 #include "../../include/htroute.h"
+#include "arch.h"
 #include "kernels.h"
 
 namespace htk {

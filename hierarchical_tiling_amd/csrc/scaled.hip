@@ -6,6 +6,7 @@
 #include <new>
 
 #include "../../include/htscaled.h"
+#include "arch.h"
 #include "scaled.h"
 
 using namespace htk;
