@@ -279,32 +279,38 @@ __device__ __forceinline__ void put_loss(const BParams& p, double dot, int n) {
 
 // 16384 x 256 fp32: sums 8 us, finish 5 us, slopes 12 us.
 //
-// Sums of the probabilities over each workgroup's tokens: a wave takes every 16th of them.
+// Sums of the probabilities over each workgroup's tokens: a wave takes every 16th of them.  Only the
+// rows that it has in hand are added in fp32; the rest is double, since a wave's rows have no limit
+// (in fp32 4 M equal rows were off by 2^-16) and the rounding of equal rows does not average out.
 template <int T, int NE>
 __global__ __launch_bounds__(kLossWaves * 64) void balance_sums(const BParams p) {
   extern __shared__ float sums[];   // [waves][experts]
   __shared__ int live[kLossWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t t0 = blockIdx.x * p.per, t1 = min(t0 + p.per, p.tokens);
-  float acc[NE];
-  static_for<NE>([&](auto i) { acc[i] = 0.f; });
+  double acc[NE];
+  static_for<NE>([&](auto i) { acc[i] = 0.0; });
   int n = 0;
   constexpr int R = rows_at_once<NE>();
   for (int64_t t = t0 + wave; t < t1; t += R * kLossWaves) {
     float v[R][NE];
     n += __popc(softmax_rows<T, NE, R>(p, t, kLossWaves, t1, lane, v));
-    static_for<R>([&](auto q) { static_for<NE>([&](auto i) { acc[i] += v[q][i]; }); });
+    static_for<NE>([&](auto i) {
+      float s = v[0][i];
+      static_for<R - 1>([&](auto q) { s += v[q + 1][i]; });
+      acc[i] += s;
+    });
   }
   static_for<NE>([&](auto i) {
-    if (lane + 64 * i < p.experts) sums[wave * p.experts + lane + 64 * i] = acc[i];
+    if (lane + 64 * i < p.experts) sums[wave * p.experts + lane + 64 * i] = (float)acc[i];
   });
   if (lane == 0) live[wave] = n;
   __syncthreads();
   static_assert(ROUTE_MAX_EXPERTS <= kLossWaves * 64, "a thread for each expert");
-  float s = 0.f;
+  double s = 0.0;
   if (tid < p.experts) {
     for (int w = 0; w < kLossWaves; ++w) s += sums[w * p.experts + tid];
-    if (gridDim.x > 1) p.partial[(int64_t)blockIdx.x * p.experts + tid] = s;
+    if (gridDim.x > 1) p.partial[(int64_t)blockIdx.x * p.experts + tid] = (float)s;
   }
   n = 0;
   for (int w = 0; w < kLossWaves; ++w) n += live[w];
@@ -317,7 +323,7 @@ __global__ __launch_bounds__(kLossWaves * 64) void balance_sums(const BParams p)
   __shared__ double dots[kLossWaves];
   double dot = 0.0;
   if (tid < p.experts) {
-    const double mean = n > 0 ? (double)s / n : 0.0;
+    const double mean = n > 0 ? s / n : 0.0;
     p.prob[tid] = (float)mean;
     dot = mean * p.counts[tid];
   }
