@@ -51,14 +51,19 @@ _lib = None
 
 def _here(s):
     """(current device, hipStream_t of `s` or of torch's current stream): by the shorter way to the
-    raw handle, since these calls are made many times a layer."""
+    raw handle, since these calls are made many times a layer.  A torch stream of another device
+    raises: a kernel on it would not reach the tensors."""
     global _raw_stream, _device
     if _raw_stream is None:
         import torch
         torch.cuda.current_stream()      # initialises the runtime if nothing has
         _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     dev = _device()
-    return dev, _raw_stream(dev) if s is None else _stream_of(s)
+    if s is None:
+        return dev, _raw_stream(dev)
+    if getattr(s, "device_index", dev) != dev:
+        raise GemmError(GEMM_ERR_INVALID_ARG, "stream")
+    return dev, _stream_of(s)
 
 
 _raw_stream = _device = None
