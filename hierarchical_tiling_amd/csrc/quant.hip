@@ -351,6 +351,14 @@ template <int XT> hipError_t launch(const QParams& p, hipStream_t s, bool* too_l
 
 bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
+// Whether every i * si + j * sj with i < n and j < m is a place of its own (strides not below 0): the
+// lines of one stride have to end before the other's next one begins.
+bool own_places(int64_t n, int64_t si, int64_t m, int64_t sj) {
+  if (n <= 1) return m <= 1 || sj > 0;
+  if (m <= 1) return si > 0;
+  return si < sj ? si > 0 && (sj - 1) / si >= n - 1 : sj > 0 && (si - 1) / sj >= m - 1;
+}
+
 }  // namespace
 }  // namespace htk
 
@@ -374,6 +382,10 @@ extern "C" int quant_blocks(const quant_args* a, void* stream) {
                                              (a->qt != nullptr) != (a->scale_t != nullptr)))
       return GEMM_ERR_INVALID_ARG;
     if (!a->x && !(a->row_index && a->x_rows == 0)) return GEMM_ERR_INVALID_ARG;
+    // scales of several blocks at one place would be written by all of them
+    const int64_t rb = (a->rows + 127) / 128, cb = (a->cols + 127) / 128;
+    if (a->scale && !own_places(block ? rb : a->rows, a->scale_r, cb, a->scale_c)) return GEMM_ERR_LAYOUT;
+    if (a->scale_t && !own_places(a->cols, a->scale_t_c, rb, a->scale_t_r)) return GEMM_ERR_LAYOUT;
   }
   const int xs = a->x_type == GEMM_F32 ? 4 : 2;
   if (!on(a->x, xs) || !on(a->scale, 4) || !on(a->scale_t, 4) || !on(a->row_index, 4)) return GEMM_ERR_MISALIGNED;

@@ -157,7 +157,8 @@ typedef struct quant_args {
 /* Enqueue the quantisation on `stream`.  With block_rows == 1, q and scale come together, as do qt
  * and scale_t; with 128, scale is required.  Nothing else of the outputs' memory is written.
  * Errors: GEMM_ERR_INVALID_ARG (also when neither q nor qt is given), GEMM_ERR_DTYPE_COMBO,
- * GEMM_ERR_LAYOUT, GEMM_ERR_MISALIGNED, GEMM_ERR_ARCH, GEMM_ERR_HIP, GEMM_ERR_LAUNCH. */
+ * GEMM_ERR_LAYOUT (also for scale strides by which blocks would share a scale's place: the larger has
+ * to pass all that the smaller spans), GEMM_ERR_MISALIGNED, GEMM_ERR_ARCH, GEMM_ERR_HIP, GEMM_ERR_LAUNCH. */
 int quant_blocks(const quant_args* args, void* stream);
 
 #ifdef __cplusplus
