@@ -278,6 +278,12 @@ def _codes(t, rows, cols):
     return None if step < 0 else (t.data_ptr(), step)
 
 
+def _padded(t, at, rows, cols):
+    """Whether the memory of codes `t` at (address, row stride) goes on behind the last row to where
+    padding it with zeros ends."""
+    return rows == 0 or cols == 0 or _bytes(t) >= (rows - 1) * at[1] + min(at[1], -(-cols // 16) * 16)
+
+
 def _scale(t, rows, cols):
     """(address, strides) of a rows x cols float32 tensor; None: another."""
     if t.shape != (rows, cols) or _TYPE_CODES.get(t.dtype, -1) != 0:
@@ -294,8 +300,8 @@ def quantize(x, q=None, scale=None, qt=None, scale_t=None, block_rows=1, pow2=Fa
     cols / 128), qt (cols, rows) and scale_t (cols, rows / 128), each any float32 strides.  With
     row_index the result has a row for each of its values.  pad: the bytes between the rows of q and
     qt up to a multiple of 16 are the caller's too (behind the last row as well) and are set to
-    zero, so that a product may count them in K.  Shapes that do not fit each other, and tensors on
-    another device than the current one, raise GemmError."""
+    zero, so that a product may count them in K.  Shapes that do not fit each other, memory that ends
+    before the padding does, and tensors on another device than the current one raise GemmError."""
     code = type_code(x)
     ok = x.dim() == 2
     if ok:
@@ -311,6 +317,8 @@ def quantize(x, q=None, scale=None, qt=None, scale_t=None, block_rows=1, pow2=Fa
         s_at = _NO_SCALE if scale is None else _scale(scale, rows if block_rows == 1 else rb, cb)
         st_at = _NO_SCALE if scale_t is None else _scale(scale_t, cols, rb)
         ok = ok and step >= 0 and q_at and qt_at and s_at and st_at
+        if ok and pad:
+            ok = (q is None or _padded(q, q_at, rows, cols)) and (qt is None or _padded(qt, qt_at, cols, rows))
     if not ok:
         raise GemmError(GEMM_ERR_INVALID_ARG, "quantize")
     a = quant_args(x.data_ptr(), code, block_rows, pow2, index_div, rows, cols, step, index,

@@ -39,6 +39,31 @@ def test_scale_of_square_blocks(rows, cols, r, c, ok, monkeypatch):
     assert status(monkeypatch, rows, cols, block_rows=128, scale_r=r, scale_c=c) == (ARCH if ok else LAYOUT)
 
 
+@pytest.mark.parametrize("rows,cols,pitch,extra", [(4, 100, 112, 12), (4, 100, 200, 12), (3, 5, 16, 11), (1, 5, 9, 4), (2, 33, 40, 7),
+                                                   (4, 96, 112, 0), (4, 100, 100, 0)])
+@pytest.mark.parametrize("turned", [False, True])
+def test_padding_behind_the_last_row(rows, cols, pitch, extra, turned, monkeypatch):
+    """On host tensors: memory that ends with the padding is taken, a byte less is refused."""
+    class Reached(Exception):
+        pass
+
+    def here(stream):
+        raise Reached
+    monkeypatch.setattr(S, "_here", here)
+    x = torch.zeros((cols, rows) if turned else (rows, cols))
+    for missing in (0, 1):
+        flat = torch.zeros(3 + (rows - 1) * pitch + cols + extra - missing, dtype=torch.uint8)
+        codes = flat[3:].as_strided((rows, cols), (pitch, 1)) if extra or not missing else None
+        if codes is None:
+            continue
+        blocks = torch.zeros(x.shape[0], -(-x.shape[1] // 128)), torch.zeros(x.shape[1], -(-x.shape[0] // 128))
+        out = dict(qt=codes, scale_t=blocks[1]) if turned else dict(q=codes, scale=blocks[0])
+        with pytest.raises(GemmError if missing else Reached):
+            S.quantize(x, pad=True, **out)
+        with pytest.raises(Reached):
+            S.quantize(x, pad=False, **out)
+
+
 @pytest.mark.gpu
 def test_expanded_scales_are_refused():
     x = torch.randn(5, 300, device="cuda")
