@@ -89,7 +89,8 @@ def _room(workspace, tokens, topk, experts, what):
 def _types():
     global _i32t, _f32t
     import torch
-    _i32t, _f32t = torch.int32, torch.float32
+    _f32t = torch.float32      # (first: another thread looks at the other)
+    _i32t = torch.int32
 
 
 _i32t = _f32t = None

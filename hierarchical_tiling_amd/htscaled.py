@@ -57,7 +57,8 @@ def _here(s):
     if _raw_stream is None:
         import torch
         torch.cuda.current_stream()      # initialises the runtime if nothing has
-        _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        _device = torch._C._cuda_getDevice           # (first: another thread looks at the other)
+        _raw_stream = torch._C._cuda_getCurrentRawStream
     dev = _device()
     if s is None:
         return dev, _raw_stream(dev)
