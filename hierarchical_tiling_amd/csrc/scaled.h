@@ -463,7 +463,8 @@ typedef __attribute__((address_space(1))) const void gbl_void_t;
 // every DMA lane has its own source address.
 //
 // Measured, two workgroups a CU: bf16 out 0.55 us for a block of a 128 x 128 tile and 0.36 us for one
-// of 64 x 128 (8192^3: 560 and 738 us), where LDS traffic and the barrier bound it; with one
+// of 64 x 128 (8192^3: 560 to 590 and 730 to 740 us; with row-major scales of A or scales of single
+// columns 632 and 644), where LDS traffic and the barrier bound it; with one
 // workgroup a CU 0.72 and 0.43.  fp32 out 1.0 us (4096 x 8192 x 5120 with scales of single columns:
 // 330 us, 1,040 TFLOP/s) is bound by issue: a wave's block of 64 x 64 has 64 matrix instructions of
 // 8 issue cycles, 128 conversions and 128 scale operations of 4.  Two workgroups of 4 waves hide each

@@ -120,10 +120,12 @@ double expected_row_tiles(const gemm_scaled_s& h, int bm) {
 
 // Predicted microseconds of a variant with k in `split` slices: rounds of workgroups at the
 // measured cost of a block, against the time that the operands' bytes take at 5.2 TB/s (the less of
-// the two counts a quarter: they overlap, not fully), plus the second kernel of a split.  Over 74
-// measured products and groups (1 to 8192 rows, 300 to 16384 columns, both output types) the choice
-// was on average 2 % above the fastest variant, 72 of them within 12 %, the worst 22 % (3000 x 3000
-// x 512); a rule on rows alone (streaming kernels up to 64 rows, k split until 512 workgroups) cost
+// the two counts a quarter: they overlap, not fully), plus the second kernel of a split.  Over 80
+// products and groups (1 to 14000 rows, 272 to 16384 columns, both output types, each kernel forced in
+// turn: profiles/scaled_choice_check.txt) the choice was on average 4 % above the fastest kernel, 71 of
+// them within 12 %; the worst, 1.4 to 1.5 times, are about 100 rows with a short k, which the streaming
+// kernels do better than predicted, a group of 440 rows whose last tile of 256 is mostly empty, and
+// fewer rows than groups.  A rule on rows alone (streaming kernels up to 64 rows, k split until 512 workgroups) cost
 // up to 2.3 times the fastest (1000 rows over 32 experts: 141 against 61 us).
 double predict(const gemm_scaled_s& h, const Variant& v, int split) {
   const gemm_scaled_desc& d = h.d;

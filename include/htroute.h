@@ -52,7 +52,8 @@ int route_experts(const route_args* args, void* stream);
  *   p = softmax(x) by rows;  prob[e] = mean of p(t, e) over the n tokens with mask[t] != 0;
  *   loss = coef * sum over e of (experts * counts[e] / (topk * n)) * prob[e]
  *
- * which is coef when all is even.  A row whose logits are all -infinity has p = 0; a NaN or a
+ * which is coef when all is even.  p is fp32; the sums over tokens are double, but for the up to four
+ * rows that are added at once and one rounding to fp32 of each wave's and workgroup's sum.  A row whose logits are all -infinity has p = 0; a NaN or a
  * +infinity in a row that counts makes the loss NaN; masked rows are not looked at.  With n == 0
  * loss and prob are 0.  live receives n. */
 typedef struct balance_args {

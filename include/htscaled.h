@@ -97,8 +97,10 @@ typedef struct gemm_scaled_args {
 /* Enqueue the product on `stream`.  Pointers need the alignment of their elements; A and B are
  * read fastest when their bases, leading dimensions and batch strides are multiples of 16 bytes
  * and K is a multiple of 16 (quant_blocks pads rows with zeros for that; a K that counts them gives
- * the same sums), with single-byte loads
- * otherwise.  M == 0 or N == 0 is a valid empty problem; K == 0 (or an empty group with
+ * the same sums), with single-byte loads otherwise (333 x 4096 x 8191: 620 us, x 8192: 28 us).  The
+ * kernel of the largest bf16 products takes A's scales with a_scale_m == 1 and B's with b_block == 128;
+ * other scale layouts of the same product run on smaller tiles (8192^3: 436 us, with a_scale_k == 1
+ * 632, with b_block == 1 644).  M == 0 or N == 0 is a valid empty problem; K == 0 (or an empty group with
  * GEMM_SCALED_K) gives D = act(beta * C + bias).  beta == 0 reads no C.  D may be C itself, with
  * the same strides.  a_scale[m] * b_scale[n] is formed in fp32 and has to be a finite, normal
  * number for the block's products to be exact to fp32; a NaN scale makes its block's outputs NaN.
