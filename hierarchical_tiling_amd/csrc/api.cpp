@@ -568,6 +568,12 @@ int check_arch() {
   return std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? GEMM_OK : GEMM_ERR_ARCH;
 }
 
+// Whether a launch can have this many workgroups along x: a dimension of one has fewer than 2^32
+// threads, and the runtime runs one with more as what is left modulo 2^32, without an error.
+bool launchable(int64_t grid, const KernelEntry& e) {
+  return grid <= INT32_MAX && grid * e.waves * 64 <= int64_t(UINT32_MAX);
+}
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 }  // namespace
@@ -952,6 +958,8 @@ int run_impl(gemm_t h, const void* A, const void* B, const void* C, void* D, con
     // rows into `batch` groups can need (each group adds at most one partial tile row); the
     // groups' tile table is built on the stream first, in the workspace
     if (!workspace || !aligned(workspace, 16)) return GEMM_ERR_INVALID_ARG;
+    grid = (int64_t(p.tiles_m) + p.batch) * p.tiles_n;
+    if (!launchable(grid, e)) return GEMM_ERR_INVALID_ARG;
     int32_t* glo = static_cast<int32_t*>(workspace);
     int64_t* gbase = reinterpret_cast<int64_t*>(static_cast<char*>(workspace) + group_lo_bytes(d.batch));
     if (launch_group_scan(offsets, (int)d.batch, d.M, e.bm, p.tiles_n, glo, gbase,
@@ -963,10 +971,9 @@ int run_impl(gemm_t h, const void* A, const void* B, const void* C, void* D, con
     p.a_row_bytes = h->a.ld * (int64_t)in_sz;
     p.c_row_bytes = d.c_stride_m * (int64_t)out_sz;
     p.d_row_bytes = d.d_stride_m * (int64_t)out_sz;
-    grid = (int64_t(p.tiles_m) + p.batch) * p.tiles_n;
     gz = 1;
   }
-  if (grid <= 0 || grid > INT32_MAX) return GEMM_ERR_INVALID_ARG;
+  if (grid <= 0 || !launchable(grid, e)) return GEMM_ERR_INVALID_ARG;
   if (sk) {
     // the tiles before the Stream-K part whole (tile order 0 .. grid - sk_tiles - 1), then the
     // persistent workgroups over the rest, then the sum of the shared tiles' pieces
@@ -1130,7 +1137,7 @@ int gemm_run_problems(gemm_t h, const gemm_problem* probs, int64_t count, const 
     total += int64_t(r.tiles_m) * r.tiles_n;
   }
   base[count] = total;
-  if (total > INT32_MAX) return GEMM_ERR_INVALID_ARG;
+  if (!launchable(total, e)) return GEMM_ERR_INVALID_ARG;
   if (total == 0) return GEMM_OK;
   void* ws = a->workspace;
   if (!ws || !aligned(ws, 16)) return GEMM_ERR_INVALID_ARG;

@@ -202,7 +202,8 @@ int gemm_workspace_size(gemm_t h, size_t* bytes);
  * K slices, then their fixed-order sum and epilogue; a Stream-K run is three: the whole tiles
  * before the Stream-K part, the persistent workgroups, then the sum of the shared tiles' pieces
  * in K order with the epilogue.  Returns after the launches are queued; launch failures
- * return GEMM_ERR_LAUNCH. */
+ * return GEMM_ERR_LAUNCH, sizes whose launch would have 2^32 threads along a dimension (2^24 tiles of
+ * 256 threads) GEMM_ERR_INVALID_ARG. */
 int gemm_run(gemm_t h, const void* A, const void* B, const void* C, void* D, const void* bias,
              float alpha, float beta, float scale_a, float scale_b, void* workspace,
              void* stream);
