@@ -125,8 +125,8 @@ double expected_row_tiles(const gemm_scaled_s& h, int bm) {
 // turn: profiles/scaled_choice_check.txt) the choice was on average 4 % above the fastest kernel, 71 of
 // them within 12 %; the worst, 1.4 to 1.5 times, are about 100 rows with a short k, which the streaming
 // kernels do better than predicted, a group of 440 rows whose last tile of 256 is mostly empty, and
-// fewer rows than groups.  A rule on rows alone (streaming kernels up to 64 rows, k split until 512 workgroups) cost
-// up to 2.3 times the fastest (1000 rows over 32 experts: 141 against 61 us).
+// fewer rows than groups.  A rule on rows alone (streaming kernels up to 64 rows, k split until 512
+// workgroups) cost up to 2.3 times the fastest (1000 rows over 32 experts: 141 against 61 us).
 double predict(const gemm_scaled_s& h, const Variant& v, int split) {
   const gemm_scaled_desc& d = h.d;
   const Cost& c = v.cost;

@@ -53,9 +53,9 @@ int route_experts(const route_args* args, void* stream);
  *   loss = coef * sum over e of (experts * counts[e] / (topk * n)) * prob[e]
  *
  * which is coef when all is even.  p is fp32; the sums over tokens are double, but for the up to four
- * rows that are added at once and one rounding to fp32 of each wave's and workgroup's sum.  A row whose logits are all -infinity has p = 0; a NaN or a
- * +infinity in a row that counts makes the loss NaN; masked rows are not looked at.  With n == 0
- * loss and prob are 0.  live receives n. */
+ * rows that are added at once and one rounding to fp32 of each wave's and workgroup's sum.  A row whose
+ * logits are all -infinity has p = 0; a NaN or a +infinity in a row that counts makes the loss NaN;
+ * masked rows are not looked at.  With n == 0 loss and prob are 0.  live receives n. */
 typedef struct balance_args {
   const void* logits;
   int32_t type;               /* GEMM_F32, GEMM_F16 or GEMM_BF16                                    */
