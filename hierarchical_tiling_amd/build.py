@@ -42,6 +42,12 @@ SOURCES = [
     ("scaled.hip", HIP),
     ("quant.hip", HIP),
     ("route.hip", HIP),
+    ("int8.hip", HIP),
+    ("int8_bf16.hip", HIP),
+    ("int8_f16.hip", HIP),
+    ("int8_f32.hip", HIP),
+    ("quant_rows.hip", HIP),
+    ("exchange.hip", HIP),
     ("api.cpp", HIP),
     ("layout.cpp", ["g++"] + COMMON),
 ]
@@ -52,11 +58,18 @@ HEADERS = [os.path.join(CSRC, "kernels.h"), os.path.join(CSRC, "pingpong.h"), os
            os.path.join(ROOT, "include", "htgemm.h"), os.path.join(ROOT, "include", "htlayout.h")]
 # headers that only some sources read, besides those
 ARCH_H = os.path.join(CSRC, "arch.h")
+INT8_H = [os.path.join(CSRC, "int8.h"), os.path.join(CSRC, "scaled.h")]
 OWN_HEADERS = {
     "api.cpp": [ARCH_H],
     "scaled.hip": [ARCH_H, os.path.join(CSRC, "scaled.h"), os.path.join(ROOT, "include", "htscaled.h")],
     "quant.hip": [ARCH_H, os.path.join(ROOT, "include", "htscaled.h")],
     "route.hip": [ARCH_H, os.path.join(ROOT, "include", "htroute.h")],
+    "exchange.hip": [ARCH_H, os.path.join(ROOT, "include", "htroute.h")],
+    "quant_rows.hip": [ARCH_H, os.path.join(ROOT, "include", "htint8.h")],
+    "int8.hip": [ARCH_H, *INT8_H, os.path.join(ROOT, "include", "htint8.h")],
+    "int8_bf16.hip": INT8_H,
+    "int8_f16.hip": INT8_H,
+    "int8_f32.hip": INT8_H,
 }
 
 

@@ -1,11 +1,13 @@
-"""ctypes binding of include/htroute.h: expert counts, offsets and row order, and the balance loss
-with its gradient, with argument marshalling only.  Every buffer is the caller's torch tensor, on
+"""ctypes binding of include/htroute.h: expert counts, offsets and row order, tokens to their experts'
+rows and back, weighted, with the gradients, and the balance loss with its gradient, with argument
+marshalling only.  Every buffer is the caller's torch tensor, on
 the current device; shapes and types that do not fit raise GemmError.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
+import struct
 
 from . import htgemm
 from .htgemm import GEMM_ERR_INVALID_ARG, GemmError, _check
@@ -32,7 +34,32 @@ class balance_grad_args(ctypes.Structure):
                 ("d_loss", _vp), ("d_logits", _vp), ("ld_d", _i64)]
 
 
-EXPORTED = ["route_workspace_size", "route_experts", "balance_loss", "balance_grad"]
+class gather_args(ctypes.Structure):
+    _fields_ = [("x", _vp), ("type", _i32), ("topk", _i32), ("tokens", _i64), ("cols", _i64), ("ldx", _i64),
+                ("order", _vp), ("slot", _vp), ("y", _vp), ("rows", _i64), ("ldy", _i64)]
+
+
+class combine_args(ctypes.Structure):
+    _fields_ = [("y", _vp), ("type", _i32), ("weight_type", _i32), ("rows", _i64), ("cols", _i64), ("ldy", _i64),
+                ("slot", _vp), ("weights", _vp), ("add", _vp), ("ld_add", _i64), ("out", _vp), ("ld_out", _i64),
+                ("tokens", _i64), ("topk", _i32)]
+
+
+class combine_grad_args(ctypes.Structure):
+    _fields_ = [("d_out", _vp), ("y", _vp), ("type", _i32), ("weight_type", _i32), ("tokens", _i64), ("rows", _i64),
+                ("cols", _i64), ("ld_out", _i64), ("ldy", _i64), ("order", _vp), ("slot", _vp), ("weights", _vp),
+                ("d_y", _vp), ("ld_dy", _i64), ("d_weights", _vp), ("topk", _i32)]
+
+
+# the same, filled by one call each
+_GATHER = struct.Struct("@P2i3q3P2q")
+_COMBINE = struct.Struct("@P2i3q3PqP2qi4x")
+_COMBINE_GRAD = struct.Struct("@2P2i5q4PqPi4x")
+assert _GATHER.size == ctypes.sizeof(gather_args) and _COMBINE.size == ctypes.sizeof(combine_args)
+assert _COMBINE_GRAD.size == ctypes.sizeof(combine_grad_args)
+
+EXPORTED = ["route_workspace_size", "route_experts", "balance_loss", "balance_grad", "route_gather", "route_combine",
+            "route_combine_grad"]
 _lib = None
 
 
@@ -46,7 +73,8 @@ def lib():
                 "route_workspace_size": [_i64, _i32, _i32, P(ctypes.c_size_t)],
                 "route_experts": [P(route_args), _vp],
                 "balance_loss": [P(balance_args), _vp],
-                "balance_grad": [P(balance_grad_args), _vp]}.items():
+                "balance_grad": [P(balance_grad_args), _vp],
+                "route_gather": [_vp, _vp], "route_combine": [_vp, _vp], "route_combine_grad": [_vp, _vp]}.items():
             f = getattr(L, name)
             f.argtypes, f.restype = args, ctypes.c_int
         _lib = L
@@ -169,3 +197,87 @@ def balance_grad(logits, counts, topk, live, d_loss, d_logits, mask=None, coef=1
     rc = (_lib or lib()).balance_grad(ctypes.byref(a), stream)
     if rc:
         raise GemmError(rc, "balance_grad")
+
+
+def _matrix(t, rows, cols, dtype):
+    """Row stride of a rows x cols tensor of a type with contiguous rows; -1 of any other."""
+    return pitch(t, rows, cols) if t.dtype is dtype and t.shape == (rows, cols) else -1
+
+
+def gather(x, order, slot, y, stream=None):
+    """route_gather: the tokens x (tokens, cols) to their experts' rows y (rows, cols), by route()'s
+    order (rows) and slot (tokens, topk); rows of no assignment become zeros.  The gradient with
+    respect to x is combine() of y's gradient without weights."""
+    if _i32t is None:
+        _types()
+    if x.dim() != 2 or slot.dim() != 2:
+        raise _bad("gather")
+    (tokens, cols), topk, rows = x.shape, slot.shape[1], order.numel()
+    ldx, ldy = pitch(x, tokens, cols), _matrix(y, rows, cols, x.dtype)
+    if ldx < 0 or ldy < 0 or not _is(order, _i32t, rows) or not _is(slot, _i32t, tokens * topk):
+        raise _bad("gather")
+    dev, stream = _here(stream)
+    if _elsewhere(dev, x, order, slot, y):
+        raise _bad("gather")
+    rc = (_lib or lib()).route_gather(_GATHER.pack(x.data_ptr(), type_code(x), topk, tokens, cols, ldx, order.data_ptr(),
+                                                   slot.data_ptr(), y.data_ptr(), rows, ldy), stream)
+    if rc:
+        raise GemmError(rc, "route_gather")
+
+
+def combine(y, slot, out, weights=None, add=None, stream=None):
+    """route_combine: the rows y (rows, cols) back to their tokens, out (tokens, cols) = add + the sum
+    of weights (tokens, topk; 1 where none are given) times y's rows at slot (tokens, topk).  out may
+    be add."""
+    if _i32t is None:
+        _types()
+    if y.dim() != 2 or slot.dim() != 2:
+        raise _bad("combine")
+    (rows, cols), (tokens, topk) = y.shape, slot.shape
+    ldy, ld_out = pitch(y, rows, cols), _matrix(out, tokens, cols, y.dtype)
+    ld_add = at = w = w_type = 0
+    if add is not None:
+        ld_add, at = _matrix(add, tokens, cols, y.dtype), add.data_ptr()
+    if weights is not None:
+        if weights.shape != slot.shape or not weights.is_contiguous():
+            raise _bad("combine")
+        w, w_type = weights.data_ptr(), type_code(weights)
+    if ldy < 0 or ld_out < 0 or ld_add < 0 or not _is(slot, _i32t, tokens * topk):
+        raise _bad("combine")
+    dev, stream = _here(stream)
+    if _elsewhere(dev, y, slot, out, weights, add):
+        raise _bad("combine")
+    rc = (_lib or lib()).route_combine(_COMBINE.pack(y.data_ptr(), type_code(y), w_type, rows, cols, ldy, slot.data_ptr(), w,
+                                                     at, ld_add, out.data_ptr(), ld_out, tokens, topk), stream)
+    if rc:
+        raise GemmError(rc, "route_combine")
+
+
+def combine_grad(d_out, y, order, slot, weights, d_y=None, d_weights=None, stream=None):
+    """route_combine_grad: the gradients of a weighted combine() from d_out (tokens, cols): d_y (rows,
+    cols) of its rows and d_weights (tokens, topk) of its weights, either of them None.  y is read for
+    d_weights only, and may be None without it."""
+    if _i32t is None:
+        _types()
+    if d_out.dim() != 2 or slot.dim() != 2 or (d_y is None and d_weights is None) or (y is None and d_weights is not None):
+        raise _bad("combine_grad")
+    (tokens, cols), topk, rows = d_out.shape, slot.shape[1], order.numel()
+    ld_out, ldy, ld_dy = pitch(d_out, tokens, cols), 0, 0
+    if y is not None:
+        ldy = _matrix(y, rows, cols, d_out.dtype)
+    if d_y is not None:
+        ld_dy = _matrix(d_y, rows, cols, d_out.dtype)
+    if (ld_out < 0 or ldy < 0 or ld_dy < 0 or not _is(order, _i32t, rows) or not _is(slot, _i32t, tokens * topk) or
+            weights.shape != slot.shape or not weights.is_contiguous() or
+            (d_weights is not None and not (_is(d_weights, weights.dtype, tokens * topk)))):
+        raise _bad("combine_grad")
+    dev, stream = _here(stream)
+    if _elsewhere(dev, d_out, y, order, slot, weights, d_y, d_weights):
+        raise _bad("combine_grad")
+    rc = (_lib or lib()).route_combine_grad(
+        _COMBINE_GRAD.pack(d_out.data_ptr(), 0 if y is None else y.data_ptr(), type_code(d_out), type_code(weights), tokens,
+                           rows, cols, ld_out, ldy, order.data_ptr(), slot.data_ptr(), weights.data_ptr(),
+                           0 if d_y is None else d_y.data_ptr(), ld_dy, 0 if d_weights is None else d_weights.data_ptr(),
+                           topk), stream)
+    if rc:
+        raise GemmError(rc, "route_combine_grad")

@@ -1,7 +1,8 @@
 /*
  * htroute.h -- C ABI of the expert routing that stands before a grouped product: which rows go to
- * which expert, in the order and with the offsets that gemm_run_grouped and gemm_scaled_run take,
- * and the loss that keeps the experts evenly used, with its gradient.
+ * which expert, in the order and with the offsets that gemm_run_grouped, gemm_scaled_run and
+ * gemm_int8_run take, the rows themselves from the tokens and back, weighted, with the gradients of
+ * both ways, and the loss that keeps the experts evenly used, with its gradient.
  *
  * Status codes and element types are those of htgemm.h.  The caller owns every device buffer and
  * the stream; calls are asynchronous; the buffers and the stream belong to the current device.
@@ -92,7 +93,75 @@ typedef struct balance_grad_args {
 } balance_grad_args;
 int balance_grad(const balance_grad_args* args, void* stream);
 
-/* Errors of all three: GEMM_ERR_INVALID_ARG, GEMM_ERR_DTYPE_COMBO, GEMM_ERR_LAYOUT,
+/* ---- tokens to their experts' rows and back --------------------------------------------------- */
+/* Up to 2^23 tokens, 2^26 rows and 2^24 columns. */
+
+/* The rows of a routing from the tokens, by order and slot of route_experts:
+ *
+ *   y(p, :) = x(order[p] / topk, :),  zeros where order[p] is outside [0, tokens * topk)
+ *
+ * Every one of the `rows` rows is written.  The result goes by order alone; slot lets a token be read
+ * once for all its rows, and may be NULL.  Its gradient is route_combine without weights. */
+typedef struct gather_args {
+  const void* x;              /* tokens x cols, row stride ldx                                      */
+  int32_t type;               /* GEMM_F32, GEMM_F16 or GEMM_BF16, of x and y                        */
+  int32_t topk;               /* 1..ROUTE_MAX_TOPK                                                  */
+  int64_t tokens, cols, ldx;
+  const int32_t* order;       /* `rows` values                                                      */
+  const int32_t* slot;        /* tokens * topk values, or NULL                                      */
+  void* y;                    /* rows x cols, row stride ldy                                        */
+  int64_t rows, ldy;
+} gather_args;
+int route_gather(const gather_args* args, void* stream);
+
+/* The tokens from the rows of a routing:
+ *
+ *   out(t, :) = add(t, :) + sum over j of weights[t * topk + j] * y(slot[t * topk + j], :)
+ *
+ * in fp32, the terms one after the other, rounded once.  Assignments whose slot is outside [0, rows)
+ * add nothing (their weight and no row is looked at); without weights every weight is 1, without add
+ * the sum starts from 0.  out may be add, with the same stride. */
+typedef struct combine_args {
+  const void* y;              /* rows x cols, row stride ldy                                        */
+  int32_t type;               /* of y, add and out                                                  */
+  int32_t weight_type;        /* GEMM_F32, GEMM_F16 or GEMM_BF16; any of them without weights       */
+  int64_t rows, cols, ldy;
+  const int32_t* slot;        /* tokens * topk values                                               */
+  const void* weights;        /* tokens * topk values, or NULL                                      */
+  const void* add;            /* tokens x cols, row stride ld_add, or NULL                          */
+  int64_t ld_add;
+  void* out;                  /* tokens x cols, row stride ld_out                                   */
+  int64_t ld_out, tokens;
+  int32_t topk;
+} combine_args;
+int route_combine(const combine_args* args, void* stream);
+
+/* Its gradients, from d_out (that of add is d_out itself):
+ *
+ *   d_y(p, :)            = weights[order[p]] * d_out(order[p] / topk, :),  zeros where order[p] is
+ *                          outside [0, tokens * topk)
+ *   d_weights[t*topk+j]  = sum over c of d_out(t, c) * y(slot[t*topk+j], c), 0 for a slot outside
+ *                          [0, rows)
+ *
+ * in fp32 in a fixed order, rounded once; d_y has the type of y, d_weights that of the weights.
+ * Either may be NULL (y is read for d_weights only).  Every row of d_y is written; it may not overlap
+ * y or d_out. */
+typedef struct combine_grad_args {
+  const void* d_out;          /* tokens x cols, row stride ld_out                                   */
+  const void* y;              /* rows x cols, row stride ldy; NULL without d_weights                */
+  int32_t type, weight_type;
+  int64_t tokens, rows, cols, ld_out, ldy;
+  const int32_t* order;       /* `rows` values; NULL without d_y                                    */
+  const int32_t* slot;        /* tokens * topk values                                               */
+  const void* weights;        /* tokens * topk values; NULL without d_y                             */
+  void* d_y;                  /* rows x cols, row stride ld_dy, or NULL                             */
+  int64_t ld_dy;
+  void* d_weights;            /* tokens * topk values, or NULL                                      */
+  int32_t topk;
+} combine_grad_args;
+int route_combine_grad(const combine_grad_args* args, void* stream);
+
+/* Errors of all: GEMM_ERR_INVALID_ARG, GEMM_ERR_DTYPE_COMBO, GEMM_ERR_LAYOUT,
  * GEMM_ERR_MISALIGNED, GEMM_ERR_ARCH, GEMM_ERR_HIP, GEMM_ERR_LAUNCH. */
 
 #ifdef __cplusplus
