@@ -30,7 +30,7 @@ struct XParams {
   const int32_t* slot;
   int64_t tokens, rows, ldx, ldy, ld_in, ld_add, ld_out;
   int64_t token_blocks;     // workgroups of the token pass
-  int cols, topk, assignments;
+  int cols, topk, assignments, row_group;
   int w_type;
 };
 
@@ -69,26 +69,40 @@ template <int VE> struct Piece {
     n = min(VE, cols);
   }
 };
-template <class T, int VE> __device__ __forceinline__ void load_piece(const T* row, const Piece<VE>& q, T (&e)[VE]) {
+// Rows are not kept in the caches: what is stored, and the rows that combine and its gradient read.
+// Stores that stay in an L2 are written back when the kernel ends, rows scattered over 1.1 GB at half the
+// rate: gather 217 us with streamed stores, 381 without (16384 tokens of 4096 to 8 of 256), and 16
+// tokens there and back 12.2 and 19.1 us; no size from 1 MB to 1 GB was better without.
+typedef u32x4 piece_t __attribute__((aligned(2)));
+template <class T, int VE, bool STREAM = false>
+__device__ __forceinline__ void load_piece(const T* row, const Piece<VE>& q, T (&e)[VE]) {
   if (q.n == VE) {
-    __builtin_memcpy(e, row + q.at, 16);
+    u32x4 w;
+    if constexpr (STREAM) w = __builtin_nontemporal_load(reinterpret_cast<const piece_t*>(row + q.at));
+    else w = *reinterpret_cast<const piece_t*>(row + q.at);
+    __builtin_memcpy(e, &w, 16);
   } else {
     static_for<VE>([&](auto i) { e[i] = i < q.n ? row[(int)i] : T(0); });
   }
 }
-template <class T, int VE> __device__ __forceinline__ void store_piece(T* row, const Piece<VE>& q, const T (&e)[VE]) {
-  if (q.first == 0 && q.n == VE) {
-    __builtin_memcpy(row + q.at, e, 16);
+// OVERLAP: the piece that the row's end cuts is stored whole, its first elements a second time with the
+// same values; not where they may have been read before (out that is add).
+template <class T, int VE, bool OVERLAP = false>
+__device__ __forceinline__ void store_piece(T* row, const Piece<VE>& q, const T (&e)[VE]) {
+  if ((OVERLAP || q.first == 0) && q.n == VE) {
+    u32x4 w;
+    __builtin_memcpy(&w, e, 16);
+    __builtin_nontemporal_store(w, reinterpret_cast<piece_t*>(row + q.at));
   } else {
     static_for<VE>([&](auto i) {
-      if (i >= q.first && i < q.n) row[q.at + i] = e[i];
+      if (i >= q.first && i < q.n) __builtin_nontemporal_store(e[i], row + q.at + i);
     });
   }
 }
 
-// The threads of a token (64, 128 or 256 of the workgroup's) and which token.
+// The token of a thread, tpt threads (whole waves) for each.
 __device__ __forceinline__ int64_t token_of(int tpt) {
-  return (int64_t)blockIdx.x * (256 / tpt) + __builtin_amdgcn_readfirstlane((int)threadIdx.x / tpt);
+  return (int64_t)blockIdx.x * (blockDim.x / tpt) + __builtin_amdgcn_readfirstlane((int)threadIdx.x / tpt);
 }
 
 // Assignment j of token t: lane j holds its slot, -1 where there is none.
@@ -98,24 +112,27 @@ __device__ __forceinline__ int lane_slot(const XParams& p, int64_t t) {
   return s < p.rows ? s : -1;     // (negative ones stay)
 }
 
-// The row pass: 16 rows a workgroup, a wave for each 4.  write(p, a) for the rows that no token owns,
-// a = -1 for a row of zeros.
-constexpr int kRowsPerBlock = 16;
-template <class F> __device__ __forceinline__ void rows_left(const XParams& p, F write) {
-  const int64_t r0 = ((int64_t)blockIdx.x - p.token_blocks) * kRowsPerBlock + (threadIdx.x >> 6) * (kRowsPerBlock / 4);
+// The row pass: row_group rows a wave.  write(p, a) for the rows that no token owns and that order
+// gives an assignment a; the others become zeros.
+template <class T, class F> __device__ __forceinline__ void rows_left(const XParams& p, F write) {
   const int lane = threadIdx.x & 63;
+  const int64_t r0 = (((int64_t)blockIdx.x - p.token_blocks) * (blockDim.x >> 6) + (threadIdx.x >> 6)) * p.row_group;
   const int64_t r = r0 + lane;
-  bool mine = lane < kRowsPerBlock / 4 && r < p.rows;
+  bool mine = lane < p.row_group && r < p.rows;
   int a = -1;
   if (mine) {
     a = p.order[r];
     if (a < 0 || a >= p.assignments) a = -1;
     else if (p.slot && p.slot[a] == r) mine = false;
   }
-  unsigned long long todo = __ballot(mine);
-  while (todo) {
+  constexpr int VE = 16 / (int)sizeof(T);
+  for (unsigned long long todo = __ballot(mine && a < 0); todo; todo &= todo - 1) {
+    T* y = (T*)p.y + (r0 + __ffsll(todo) - 1) * p.ldy;
+    T zero[VE] = {};
+    for (int c = lane * VE; c < p.cols; c += 64 * VE) store_piece<T, VE, true>(y, Piece<VE>(c, p.cols), zero);
+  }
+  for (unsigned long long todo = __ballot(mine && a >= 0); todo; todo &= todo - 1) {
     const int l = __ffsll(todo) - 1;
-    todo &= todo - 1;
     write(r0 + l, __builtin_amdgcn_readlane(a, l));
   }
 }
@@ -127,43 +144,46 @@ template <class T> __device__ __forceinline__ const T* row_at(const void* base, 
 // ---- gather --------------------------------------------------------------------------------
 // Elements are moved, not looked at: XT is DT_F32 or a 16-bit type.
 template <int XT>
-__global__ __launch_bounds__(256) void gather_rows(const XParams p, int tpt) {
+__global__ __launch_bounds__(1024) void gather_rows(const XParams p, int tpt) {
   typedef typename El<XT>::T T;
   constexpr int VE = El<XT>::VE, U = 2;
   const int lane = threadIdx.x & 63;
   if ((int64_t)blockIdx.x >= p.token_blocks) {
-    rows_left(p, [&](int64_t r, int a) {
+    rows_left<T>(p, [&](int64_t r, int a) {
       T* y = (T*)p.y + r * p.ldy;
-      const T* x = row_at<T>(p.x, a < 0 ? 0 : a / p.topk, p.ldx);
+      const T* x = row_at<T>(p.x, a / p.topk, p.ldx);
       for (int c = lane * VE; c < p.cols; c += 64 * VE) {
         const Piece<VE> q(c, p.cols);
         alignas(16) T e[VE];
-        static_for<VE>([&](auto i) { e[i] = T(0); });
-        if (a >= 0) load_piece<T, VE>(x, q, e);
-        store_piece<T, VE>(y, q, e);
+        load_piece<T, VE>(x, q, e);
+        store_piece<T, VE, true>(y, q, e);
       }
     });
     return;
   }
   const int64_t t = token_of(tpt);
   if (t >= p.tokens) return;
-  int s = lane_slot(p, t);
-  if (s >= 0 && p.order[s] != t * p.topk + lane) s = -1;     // another's row
-  const unsigned long long live = __ballot(s >= 0);
-  if (!live) return;
   const T* x = row_at<T>(p.x, t, p.ldx);
   const int tid = threadIdx.x % tpt;
-  for (int c0 = 0; c0 < p.cols; c0 += tpt * VE * U) {
-    alignas(16) T e[U][VE];
+  alignas(16) T e[U][VE];
+  auto load = [&](int c0) {
     static_for<U>([&](auto u) {
       const int c = c0 + (u * tpt + tid) * VE;
       if (c < p.cols) load_piece<T, VE>(x, Piece<VE>(c, p.cols), e[u]);
     });
+  };
+  load(0);                      // on its way while the slots and the order are looked at
+  int s = lane_slot(p, t);
+  if (s >= 0 && p.order[s] != t * p.topk + lane) s = -1;     // another's row
+  const unsigned long long live = __ballot(s >= 0);
+  if (!live) return;
+  for (int c0 = 0; c0 < p.cols; c0 += tpt * VE * U) {
+    if (c0 > 0) load(c0);
     for (unsigned long long todo = live; todo; todo &= todo - 1) {
       T* y = (T*)p.y + (int64_t)__builtin_amdgcn_readlane(s, __ffsll(todo) - 1) * p.ldy;
       static_for<U>([&](auto u) {
         const int c = c0 + (u * tpt + tid) * VE;
-        if (c < p.cols) store_piece<T, VE>(y, Piece<VE>(c, p.cols), e[u]);
+        if (c < p.cols) store_piece<T, VE, true>(y, Piece<VE>(c, p.cols), e[u]);
       });
     }
   }
@@ -181,7 +201,7 @@ __device__ __forceinline__ void add_terms(const XParams& p, int s, float w, unsi
   static_for<B>([&](auto b) {
     const int j = __ffsll(todo) - 1;
     todo &= todo - 1;
-    load_piece<T, VE>(row_at<T>(p.rows_in, __builtin_amdgcn_readlane(s, j), p.ld_in), q, e[b]);
+    load_piece<T, VE, true>(row_at<T>(p.rows_in, __builtin_amdgcn_readlane(s, j), p.ld_in), q, e[b]);
     if constexpr (W) f[b] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), j));
   });
   static_for<B>([&](auto b) {
@@ -193,7 +213,7 @@ __device__ __forceinline__ void add_terms(const XParams& p, int s, float w, unsi
 }
 
 template <int XT, bool W>
-__global__ __launch_bounds__(256) void combine_rows(const XParams p, int tpt) {
+__global__ __launch_bounds__(1024) void combine_rows(const XParams p, int tpt) {
   typedef typename El<XT>::T T;
   constexpr int VE = El<XT>::VE;
   const int64_t t = token_of(tpt);
@@ -256,7 +276,7 @@ __device__ __forceinline__ void grad_terms(const XParams& p, const typename El<X
     const Piece<VE> q(c, p.cols);
     alignas(16) T d[VE], e[DW ? B : 1][VE];
     load_piece<T, VE>(d_out, q, d);
-    if constexpr (DW) static_for<B>([&](auto b) { load_piece<T, VE>(row_at<T>(p.rows_in, at[b], p.ld_in), q, e[b]); });
+    if constexpr (DW) static_for<B>([&](auto b) { load_piece<T, VE, true>(row_at<T>(p.rows_in, at[b], p.ld_in), q, e[b]); });
     float v[VE];
     static_for<VE>([&](auto i) { v[i] = El<XT>::up(d[i]); });
     if constexpr (DY) {
@@ -264,7 +284,7 @@ __device__ __forceinline__ void grad_terms(const XParams& p, const typename El<X
         if (own >> j[b] & 1) {
           alignas(16) T o[VE];
           static_for<VE>([&](auto i) { o[i] = El<XT>::down(f[b] * v[i]); });
-          store_piece<T, VE>((T*)p.y + (int64_t)at[b] * p.ldy, q, o);
+          store_piece<T, VE, true>((T*)p.y + (int64_t)at[b] * p.ldy, q, o);
         }
       });
     }
@@ -289,25 +309,22 @@ __device__ __forceinline__ void grad_terms(const XParams& p, const typename El<X
 }
 
 template <int XT, bool DY, bool DW>
-__global__ __launch_bounds__(256) void combine_rows_grad(const XParams p, int tpt) {
+__global__ __launch_bounds__(1024) void combine_rows_grad(const XParams p, int tpt) {
   typedef typename El<XT>::T T;
   constexpr int VE = El<XT>::VE;
-  __shared__ float sums[4][64];         // of each wave, by assignment
+  __shared__ float sums[16][64];         // of each wave, by assignment
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if ((int64_t)blockIdx.x >= p.token_blocks) {
-    rows_left(p, [&](int64_t r, int a) {
+    rows_left<T>(p, [&](int64_t r, int a) {
       T* y = (T*)p.y + r * p.ldy;
-      const T* d = row_at<T>(p.x, a < 0 ? 0 : a / p.topk, p.ldx);
-      const float f = a < 0 ? 0.f : weight(p, a);
+      const T* d = row_at<T>(p.x, a / p.topk, p.ldx);
+      const float f = weight(p, a);
       for (int c = lane * VE; c < p.cols; c += 64 * VE) {
         const Piece<VE> q(c, p.cols);
         alignas(16) T e[VE];
-        static_for<VE>([&](auto i) { e[i] = T(0); });
-        if (a >= 0) {
-          load_piece<T, VE>(d, q, e);
-          static_for<VE>([&](auto i) { e[i] = El<XT>::down(f * El<XT>::up(e[i])); });
-        }
-        store_piece<T, VE>(y, q, e);
+        load_piece<T, VE>(d, q, e);
+        static_for<VE>([&](auto i) { e[i] = El<XT>::down(f * El<XT>::up(e[i])); });
+        store_piece<T, VE, true>(y, q, e);
       }
     });
     return;
@@ -338,10 +355,26 @@ __global__ __launch_bounds__(256) void combine_rows_grad(const XParams p, int tp
 }
 
 // ---- launch --------------------------------------------------------------------------------
-// Threads for each token: enough for two pieces each, a wave at least and a workgroup at most.
-int threads_of(int64_t cols, int ve) {
+struct Shape {
+  int tpt, threads;         // threads for each token, and of a workgroup
+  int64_t token_blocks, row_blocks;
+  int row_group;
+};
+// Threads for each token: two pieces each, a wave at least and four at most; while there are fewer
+// tokens than CUs, one piece each and up to 16 waves, as a chain of loads and stores is then what
+// counts.  The row pass looks at 4 rows a wave, at 1 while that makes few workgroups.
+Shape shape_of(int64_t tokens, int64_t rows, int64_t cols, int ve) {
   const int64_t pieces = (cols + ve - 1) / ve;
-  return pieces <= 128 ? 64 : pieces <= 256 ? 128 : 256;
+  Shape s;
+  const int64_t want = tokens <= 256 ? pieces : (pieces + 1) / 2, most = tokens <= 256 ? 1024 : 256;
+  s.tpt = 64;
+  while (s.tpt < want && s.tpt < most) s.tpt *= 2;
+  s.threads = std::max(s.tpt, 256);
+  s.token_blocks = (tokens * s.tpt + s.threads - 1) / s.threads;
+  s.row_group = rows <= 4096 ? 1 : 4;
+  const int64_t per = s.threads / 64 * s.row_group;
+  s.row_blocks = (rows + per - 1) / per;
+  return s;
 }
 
 bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -349,7 +382,7 @@ bool known(int type) { return type == GEMM_F32 || type == GEMM_F16 || type == GE
 int size_of(int type) { return type == GEMM_F32 ? 4 : 2; }
 
 // Sizes that all three share.  Assignments and rows are 32-bit numbers, and a launch has fewer than
-// 2^32 threads: a workgroup of 256 for each token, and one for each 16 rows.
+// 2^32 threads: 256 at most for each token, and a wave for each 4 rows.
 constexpr int64_t kMostTokens = int64_t(1) << 23, kMostRows = int64_t(1) << 26, kMostCols = int64_t(1) << 24;
 int check(int64_t tokens, int64_t rows, int64_t cols, int topk, int type) {
   if (tokens < 0 || rows < 0 || cols < 0 || tokens > kMostTokens || rows > kMostRows || cols > kMostCols)
@@ -390,12 +423,13 @@ int route_gather(const gather_args* a, void* stream) {
   p.cols = (int)a->cols;
   p.topk = a->topk;
   p.assignments = (int)(a->tokens * a->topk);
-  const int tpt = threads_of(a->cols, 16 / size);
-  p.token_blocks = a->slot ? (a->tokens * tpt + 255) / 256 : 0;
-  const dim3 grid((unsigned)(p.token_blocks + (a->rows + kRowsPerBlock - 1) / kRowsPerBlock));
+  const Shape h = shape_of(a->tokens, a->rows, a->cols, 16 / size);
+  p.token_blocks = a->slot ? h.token_blocks : 0;
+  p.row_group = h.row_group;
+  const dim3 grid((unsigned)(p.token_blocks + h.row_blocks)), block(h.threads);
   hipStream_t s = (hipStream_t)stream;
-  if (a->type == GEMM_F32) hipLaunchKernelGGL(gather_rows<DT_F32>, grid, dim3(256), 0, s, p, tpt);
-  else hipLaunchKernelGGL(gather_rows<DT_BF16>, grid, dim3(256), 0, s, p, tpt);
+  if (a->type == GEMM_F32) hipLaunchKernelGGL(gather_rows<DT_F32>, grid, block, 0, s, p, h.tpt);
+  else hipLaunchKernelGGL(gather_rows<DT_BF16>, grid, block, 0, s, p, h.tpt);
   return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
@@ -428,12 +462,12 @@ int route_combine(const combine_args* a, void* stream) {
   p.ld_out = a->ld_out;
   p.cols = (int)a->cols;
   p.topk = a->topk;
-  const int tpt = threads_of(a->cols, 16 / size);
-  const dim3 grid((unsigned)((a->tokens * tpt + 255) / 256));
+  const Shape h = shape_of(a->tokens, 0, a->cols, 16 / size);
+  const dim3 grid((unsigned)h.token_blocks), block(h.threads);
   hipStream_t s = (hipStream_t)stream;
   auto go = [&](auto xt) {
-    if (a->weights) hipLaunchKernelGGL((combine_rows<decltype(xt)::value, true>), grid, dim3(256), 0, s, p, tpt);
-    else hipLaunchKernelGGL((combine_rows<decltype(xt)::value, false>), grid, dim3(256), 0, s, p, tpt);
+    if (a->weights) hipLaunchKernelGGL((combine_rows<decltype(xt)::value, true>), grid, block, 0, s, p, h.tpt);
+    else hipLaunchKernelGGL((combine_rows<decltype(xt)::value, false>), grid, block, 0, s, p, h.tpt);
   };
   if (a->type == GEMM_F32) go(std::integral_constant<int, DT_F32>{});
   else if (a->type == GEMM_F16) go(std::integral_constant<int, DT_F16>{});
@@ -475,15 +509,16 @@ int route_combine_grad(const combine_grad_args* a, void* stream) {
   p.cols = (int)a->cols;
   p.topk = a->topk;
   p.assignments = (int)(a->tokens * a->topk);
-  const int tpt = threads_of(a->cols, 16 / size);
-  p.token_blocks = (a->tokens * tpt + 255) / 256;
-  const dim3 grid((unsigned)(p.token_blocks + (dy ? (a->rows + kRowsPerBlock - 1) / kRowsPerBlock : 0)));
+  const Shape h = shape_of(a->tokens, a->rows, a->cols, 16 / size);
+  p.token_blocks = h.token_blocks;
+  p.row_group = h.row_group;
+  const dim3 grid((unsigned)(h.token_blocks + (dy ? h.row_blocks : 0))), block(h.threads);
   hipStream_t s = (hipStream_t)stream;
   auto go = [&](auto xt) {
     constexpr int XT = decltype(xt)::value;
-    if (dy && dw) hipLaunchKernelGGL((combine_rows_grad<XT, true, true>), grid, dim3(256), 0, s, p, tpt);
-    else if (dy) hipLaunchKernelGGL((combine_rows_grad<XT, true, false>), grid, dim3(256), 0, s, p, tpt);
-    else hipLaunchKernelGGL((combine_rows_grad<XT, false, true>), grid, dim3(256), 0, s, p, tpt);
+    if (dy && dw) hipLaunchKernelGGL((combine_rows_grad<XT, true, true>), grid, block, 0, s, p, h.tpt);
+    else if (dy) hipLaunchKernelGGL((combine_rows_grad<XT, true, false>), grid, block, 0, s, p, h.tpt);
+    else hipLaunchKernelGGL((combine_rows_grad<XT, false, true>), grid, block, 0, s, p, h.tpt);
   };
   if (a->type == GEMM_F32) go(std::integral_constant<int, DT_F32>{});
   else if (a->type == GEMM_F16) go(std::integral_constant<int, DT_F16>{});
