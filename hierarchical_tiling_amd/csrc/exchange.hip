@@ -355,20 +355,28 @@ __global__ __launch_bounds__(1024) void combine_rows_grad(const XParams p, int t
 }
 
 // ---- launch --------------------------------------------------------------------------------
+// Sizes that all three share.  Assignments and rows are 32-bit numbers, and a launch has fewer than
+// 2^32 threads: up to 2^31 for the tokens, and a wave for each 4 rows (2^30).
+constexpr int64_t kMostTokens = int64_t(1) << 23, kMostRows = int64_t(1) << 26, kMostCols = int64_t(1) << 24;
+constexpr int64_t kMostThreads = int64_t(1) << 31;
+
 struct Shape {
   int tpt, threads;         // threads for each token, and of a workgroup
   int64_t token_blocks, row_blocks;
   int row_group;
 };
-// Threads for each token: two pieces each, a wave at least and four at most; while there are fewer
-// tokens than CUs, one piece each and up to 16 waves, as a chain of loads and stores is then what
-// counts.  The row pass looks at 4 rows a wave, at 1 while that makes few workgroups.
-Shape shape_of(int64_t tokens, int64_t rows, int64_t cols, int ve) {
+// Threads for each token: one for each piece, a wave at least and `most` threads at most.  Combine takes
+// up to 1024 (16384 x 4096 bf16 196 us, with two pieces a thread 204; 500 x 7000 f32 14 and 23), gather
+// 1024 for up to 256 tokens, when its chain of loads and stores counts (37 x 2051 f16 3.8 us, with 256
+// threads 7.6), and 256 for more (300 x 4096 5.0 us, with 1024 5.6; 500 x 7000 f32 15.3 and 17.5).  The
+// gradient, which joins its threads' sums, takes 1024 for up to 1024 tokens and 256 for more: 500 x 7000
+// f32 31 us and 38, 16384 x 2048 f32 219 and 210.  The row pass looks at 4 rows a wave, at 1 while that
+// makes few workgroups.
+Shape shape_of(int64_t tokens, int64_t rows, int64_t cols, int ve, int most) {
   const int64_t pieces = (cols + ve - 1) / ve;
   Shape s;
-  const int64_t want = tokens <= 256 ? pieces : (pieces + 1) / 2, most = tokens <= 256 ? 1024 : 256;
   s.tpt = 64;
-  while (s.tpt < want && s.tpt < most) s.tpt *= 2;
+  while (s.tpt < pieces && s.tpt < most && tokens * s.tpt < kMostThreads / 2) s.tpt *= 2;
   s.threads = std::max(s.tpt, 256);
   s.token_blocks = (tokens * s.tpt + s.threads - 1) / s.threads;
   s.row_group = rows <= 4096 ? 1 : 4;
@@ -381,9 +389,6 @@ bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a 
 bool known(int type) { return type == GEMM_F32 || type == GEMM_F16 || type == GEMM_BF16; }
 int size_of(int type) { return type == GEMM_F32 ? 4 : 2; }
 
-// Sizes that all three share.  Assignments and rows are 32-bit numbers, and a launch has fewer than
-// 2^32 threads: 256 at most for each token, and a wave for each 4 rows.
-constexpr int64_t kMostTokens = int64_t(1) << 23, kMostRows = int64_t(1) << 26, kMostCols = int64_t(1) << 24;
 int check(int64_t tokens, int64_t rows, int64_t cols, int topk, int type) {
   if (tokens < 0 || rows < 0 || cols < 0 || tokens > kMostTokens || rows > kMostRows || cols > kMostCols)
     return GEMM_ERR_INVALID_ARG;
@@ -423,7 +428,7 @@ int route_gather(const gather_args* a, void* stream) {
   p.cols = (int)a->cols;
   p.topk = a->topk;
   p.assignments = (int)(a->tokens * a->topk);
-  const Shape h = shape_of(a->tokens, a->rows, a->cols, 16 / size);
+  const Shape h = shape_of(a->tokens, a->rows, a->cols, 16 / size, a->tokens <= 256 ? 1024 : 256);
   p.token_blocks = a->slot ? h.token_blocks : 0;
   p.row_group = h.row_group;
   const dim3 grid((unsigned)(p.token_blocks + h.row_blocks)), block(h.threads);
@@ -462,7 +467,7 @@ int route_combine(const combine_args* a, void* stream) {
   p.ld_out = a->ld_out;
   p.cols = (int)a->cols;
   p.topk = a->topk;
-  const Shape h = shape_of(a->tokens, 0, a->cols, 16 / size);
+  const Shape h = shape_of(a->tokens, 0, a->cols, 16 / size, 1024);
   const dim3 grid((unsigned)h.token_blocks), block(h.threads);
   hipStream_t s = (hipStream_t)stream;
   auto go = [&](auto xt) {
@@ -509,7 +514,7 @@ int route_combine_grad(const combine_grad_args* a, void* stream) {
   p.cols = (int)a->cols;
   p.topk = a->topk;
   p.assignments = (int)(a->tokens * a->topk);
-  const Shape h = shape_of(a->tokens, a->rows, a->cols, 16 / size);
+  const Shape h = shape_of(a->tokens, a->rows, a->cols, 16 / size, a->tokens <= 1024 ? 1024 : 256);
   p.token_blocks = h.token_blocks;
   p.row_group = h.row_group;
   const dim3 grid((unsigned)(h.token_blocks + (dy ? h.row_blocks : 0))), block(h.threads);
