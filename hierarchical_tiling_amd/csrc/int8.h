@@ -52,21 +52,35 @@ __device__ __forceinline__ float scaled_sum(int sum, float sa, float sb) { retur
 
 // ------------------------------------------------------------------------------------------
 // Outputs.  A lane has RM rows and in each RN pieces of 4 columns, dealt as Cols says, so that VO
-// outputs are 16 bytes of D.  Waves whose columns all lie below N store 16-byte pieces at any
-// alignment (the memory system splits those that cross a line); there is one straight copy of the
-// code for each activation and for C or none.  The others go element by element, a row block at a
-// time through LDS, a lane for each column.  With k in slices the integer sums go to the slice's plane.
+// outputs are 16 bytes of D, loaded (C) and stored as one piece at any alignment (the memory system
+// splits those that cross a line).  Waves whose columns all lie below N have a straight copy of the
+// code for each activation and for C or none; in the others (EDGE) a piece that N cuts goes element by
+// element.  Nothing but C is loaded between the stores: a wave waits for its stores before it sees a
+// later load (an edge path that took row blocks through LDS cost the 6 workgroups of the last columns
+// 6 us: 333 x 4064 x 8192 31.9 us in place of 25.7).  With k in slices the integer sums go to the
+// slice's plane.
 // ------------------------------------------------------------------------------------------
-template <class OT, int RM, int RN, int ACT, bool HAS_C, class RowOf>
+template <class OT, int RM, int RN, int ACT, bool HAS_C, bool EDGE, class RowOf>
 __device__ __forceinline__ void store_pieces(const SParams& p, const STile& s, const i32x4 (&acc)[RM][RN],
                                              const float (&sa)[RM], const f32x4 (&sb)[RN], RowOf row_of, int64_t col,
                                              int x) {
   typedef Cols<OT> CM;
   constexpr int VO = CM::VO, NQ = RN / CM::JP, RG = RM % 2 == 0 ? 2 : 1;
+  // columns of piece q below N, and 16 bytes of it from `base` on, those past N as the last column
+  auto left = [&](int q) { return EDGE ? (int)min(p.N - col - CM::of(q * CM::JP, 0), (int64_t)VO) : VO; };
+  auto piece = [&](const void* base, int64_t row, int64_t ld, int q) {
+    const OT* src = (const OT*)base + row * ld + col + CM::of(q * CM::JP, 0);
+    if (!EDGE || left(q) == VO) return load16(src);
+    alignas(16) OT e[VO];
+    static_for<VO>([&](auto i) { e[i] = i < left(q) ? src[(int)i] : OT(0); });
+    u32x4 w;
+    __builtin_memcpy(&w, e, 16);
+    return w;
+  };
   u32x4 bias[NQ];
   static_for<NQ>([&](auto q) {
     bias[q] = u32x4{0, 0, 0, 0};
-    if (p.bias) bias[q] = load16((const OT*)p.bias + col + CM::of(q * CM::JP, 0));
+    if (p.bias) bias[q] = piece(p.bias, 0, 0, q);
   });
   // RG row blocks at a time, whose C is loaded before they are stored: D may be C, and more in hand at
   // once would not fit the registers
@@ -77,7 +91,7 @@ __device__ __forceinline__ void store_pieces(const SParams& p, const STile& s, c
       static_for<NQ>([&](auto q) {
         c[h][q] = u32x4{0, 0, 0, 0};
         if constexpr (HAS_C)
-          if (row < s.M) c[h][q] = load16((const OT*)s.C + row * p.ldc + col + CM::of(q * CM::JP, 0));
+          if (row < s.M) c[h][q] = piece(s.C, row, p.ldc, q);
       });
     });
     static_for<RG>([&](auto h) {
@@ -92,9 +106,16 @@ __device__ __forceinline__ void store_pieces(const SParams& p, const STile& s, c
             float y = scaled_sum(acc[i][j][r], sa[i], sb[j][r]) * p.alpha;
             if constexpr (HAS_C) y += p.beta * SOut<OT>::load(&c[h][q], e);
             y += SOut<OT>::load(&bias[q], e);
-            o[e] = SOut<OT>::bits(ACT == 1 ? relu(y) : ACT == 2 ? gelu(y) : ACT == 3 ? silu(y) : y);
+            o[e] = SOut<OT>::bits(ACT < 0 ? activate(p.act, y) : ACT == 1 ? relu(y) : ACT == 2 ? gelu(y) : ACT == 3 ? silu(y) : y);
           });
-          __builtin_memcpy(d + CM::of(q * CM::JP, 0), o, 16);
+          OT* to = d + CM::of(q * CM::JP, 0);
+          if (!EDGE || left(q) == VO) {
+            __builtin_memcpy(to, o, 16);
+          } else {
+            static_for<VO>([&](auto e) {
+              if (e < left(q)) to[(int)e] = o[e];
+            });
+          }
         });
       }
     });
@@ -102,80 +123,55 @@ __device__ __forceinline__ void store_pieces(const SParams& p, const STile& s, c
 }
 
 // col0: the wave's first column (at or past N for a wave that stores nothing); row_of(i, x): the row
-// of row block i in lane x = lane % 16.  `lds`: the kernel's LDS, at least 16 x 68 floats a wave.
+// of row block i in lane x = lane % 16.
 template <class OT, int RM, int RN, class RowOf>
 __device__ __forceinline__ void store_sums(const SParams& p, const STile& s, const i32x4 (&acc)[RM][RN], RowOf row_of,
-                                           int64_t col0, u32x4* lds, int wave) {
+                                           int64_t col0) {
   typedef Cols<OT> CM;
   const int lane = threadIdx.x & 63, x = lane & 15, c4 = lane >> 4;
-  __syncthreads();              // the operands in LDS have been read
   if (col0 >= p.N) return;
   const bool whole = col0 + 16 * RN <= p.N;
-  if (whole && p.split_k > 1) {
+  if (p.split_k > 1) {
     int* plane = reinterpret_cast<int*>(p.workspace) + (int64_t)blockIdx.y * p.M * p.N + col0;
     static_for<RM>([&](auto i) {
       const int64_t row = row_of(i, x);
-      if (row < s.M) static_for<RN>([&](auto j) { __builtin_memcpy(plane + row * p.N + CM::of(j, c4), &acc[i][j], 16); });
+      if (row < s.M) {
+        static_for<RN>([&](auto j) {
+          int* to = plane + row * p.N + CM::of(j, c4);
+          const int64_t left = p.N - col0 - CM::of(j, c4);
+          if (left >= 4) __builtin_memcpy(to, &acc[i][j], 16);
+          else static_for<4>([&](auto r) {
+            if (r < left) to[(int)r] = acc[i][j][(int)r];
+          });
+        });
+      }
     });
     return;
   }
-  if (whole) {
-    float sa[RM];
-    f32x4 sb[RN];
-    static_for<RM>([&](auto i) { sa[i] = 0.f; });
-    static_for<RN>([&](auto j) { sb[j] = f32x4{}; });
-    if (p.K > 0) {              // a product without k reads no scales
-      static_for<RN>([&](auto j) { __builtin_memcpy(&sb[j], s.b_scale + col0 + CM::of(j, c4), 16); });
-      static_for<RM>([&](auto i) { sa[i] = s.a_scale[min(row_of(i, x), s.M - 1)]; });
-    }
-    const int64_t col = col0 + CM::of(0, c4);
-    auto go = [&](auto act) {
-      if (s.C) store_pieces<OT, RM, RN, decltype(act)::value, true>(p, s, acc, sa, sb, row_of, col, x);
-      else store_pieces<OT, RM, RN, decltype(act)::value, false>(p, s, acc, sa, sb, row_of, col, x);
-    };
-    if (p.act == 0) go(std::integral_constant<int, 0>{});
-    else if (p.act == 3) go(std::integral_constant<int, 3>{});
-    else if (p.act == 2) go(std::integral_constant<int, 2>{});
-    else go(std::integral_constant<int, 1>{});
-    return;
+  float sa[RM];
+  f32x4 sb[RN];
+  static_for<RM>([&](auto i) { sa[i] = 0.f; });
+  static_for<RN>([&](auto j) { sb[j] = f32x4{}; });
+  if (p.K > 0) {                // a product without k reads no scales
+    static_for<RN>([&](auto j) {
+      const int64_t n = col0 + CM::of(j, c4);
+      if (whole) __builtin_memcpy(&sb[j], s.b_scale + n, 16);
+      else static_for<4>([&](auto r) { sb[j][(int)r] = s.b_scale[min(n + r, p.N - 1)]; });
+    });
+    static_for<RM>([&](auto i) { sa[i] = s.a_scale[min(row_of(i, x), s.M - 1)]; });
   }
-  constexpr int W = 16 * RN, PITCH = W + 4, U = 8;
-  static_assert(W == 64, "a lane for each column");
-  int* mine = reinterpret_cast<int*>(lds) + wave * 16 * PITCH;
-  const int64_t col = col0 + lane;
-  const bool in = col < p.N, scaled = p.K > 0 && p.split_k <= 1;
-  const float bias = p.bias && in ? SOut<OT>::load(p.bias, col) : 0.f;
-  const float sb = scaled ? s.b_scale[min(col, p.N - 1)] : 0.f;
-  int* plane = p.split_k > 1 ? reinterpret_cast<int*>(p.workspace) + (int64_t)blockIdx.y * p.M * p.N : nullptr;
-  static_for<RM>([&](auto i) {
-    static_for<RN>([&](auto j) { *reinterpret_cast<i32x4*>(&mine[x * PITCH + CM::of(j, c4)]) = acc[i][j]; });
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll 1
-    for (int r0 = 0; r0 < 16; r0 += U) {
-      int v[U];
-      float c[U], sa[U];
-      static_for<U>([&](auto u) {
-        const int64_t row = row_of(i, r0 + u);
-        const bool ok = in && row < s.M;
-        v[u] = mine[(r0 + u) * PITCH + lane];
-        c[u] = s.C && ok ? SOut<OT>::load(s.C, row * p.ldc + col) : 0.f;
-        sa[u] = scaled && ok ? s.a_scale[row] : 0.f;
-      });
-      static_for<U>([&](auto u) {
-        const int64_t row = row_of(i, r0 + u);
-        if (in && row < s.M) {
-          if (plane) {
-            plane[row * p.N + col] = v[u];
-          } else {
-            float t = scaled_sum(v[u], sa[u], sb) * p.alpha;
-            if (s.C) t += p.beta * c[u];
-            ((OT*)s.D)[row * p.ldd + col] = SOut<OT>::bits(activate(p.act, t + bias));
-          }
-        }
-      });
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  });
+  const int64_t col = col0 + CM::of(0, c4);
+  auto go = [&](auto act, auto edge) {
+    constexpr int A = decltype(act)::value;
+    constexpr bool E = decltype(edge)::value;
+    if (s.C) store_pieces<OT, RM, RN, A, true, E>(p, s, acc, sa, sb, row_of, col, x);
+    else store_pieces<OT, RM, RN, A, false, E>(p, s, acc, sa, sb, row_of, col, x);
+  };
+  if (!whole) go(std::integral_constant<int, -1>{}, std::true_type{});
+  else if (p.act == 0) go(std::integral_constant<int, 0>{}, std::false_type{});
+  else if (p.act == 3) go(std::integral_constant<int, 3>{}, std::false_type{});
+  else if (p.act == 2) go(std::integral_constant<int, 2>{}, std::false_type{});
+  else go(std::integral_constant<int, 1>{}, std::false_type{});
 }
 
 // One output from its sum.
@@ -277,7 +273,7 @@ __global__ __launch_bounds__(256, OCC) void i8_any(const SParams p) {
       static_for<RM>([&](auto i) { static_for<RN>([&](auto j) { mma_i8(acc[i][j], fb[j], fa[i]); }); });
     });
   }
-  store_sums<OT, RM, RN>(p, s, acc, [&](int i, int r) { return s.m0 + wm * TM + r * RM + i; }, s.n0 + wn * TN, lds, wave);
+  store_sums<OT, RM, RN>(p, s, acc, [&](int i, int r) { return s.m0 + wm * TM + r * RM + i; }, s.n0 + wn * TN);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -386,7 +382,7 @@ __global__ __launch_bounds__(KH * WM * WN * 64, OCC) void i8_tile(const SParams 
     if (half == 0) static_for<RM>([&](auto i) { static_for<RN>([&](auto j) { acc[i][j] += sums[(i * RN + j) * 64]; }); });
   }
   store_sums<OT, RM, RN>(p, s, acc, [&](int i, int r) { return s.m0 + wm * TM + r * RM + i; },
-                         half == 0 ? s.n0 + wn * TN : p.N, lds, wave);
+                         half == 0 ? s.n0 + wn * TN : p.N);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -571,15 +567,17 @@ __global__ __launch_bounds__(512, 1) void i8_pp(const SParams p) {
         static_for<2>([&](auto u) { static_for<RM>([&](auto i) { fa[u][i] = keep_bytes(fa[u][i], cut - (c4 + 4 * u) * 16); }); });
       wait_counts<8, true>();
       phase_end();
+      __builtin_amdgcn_s_setprio(1);     // the computing wave before the one that reads
       static_for<2>([&](auto u) {
         static_for<RM>([&](auto i) { static_for<RN>([&](auto j) { mma_i8(acc[i][j], fb[u][j], fa[u][i]); }); });
       });
+      __builtin_amdgcn_s_setprio(0);
       phase_end();
     }
     if (g == 0) phase_end();
     wait_counts<0, true>();     // zero blocks issued past the end
   }
-  store_sums<OT, RM, RN>(p, s, acc, [&](int i, int r) { return s.m0 + g * 128 + r * 8 + i; }, s.n0 + wq * 64, lds, wave);
+  store_sums<OT, RM, RN>(p, s, acc, [&](int i, int r) { return s.m0 + g * 128 + r * 8 + i; }, s.n0 + wq * 64);
 }
 
 // The planes of a split k, added, and the epilogue.
