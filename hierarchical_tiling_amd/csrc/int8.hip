@@ -29,17 +29,17 @@ struct Variant {
 };
 
 const Variant kVariants[] = {
-    {"any_64x128", 64, 128, 4, 2 * 192 * 128, 1, {2, 1, .9f, 1.3f, 2.f}},
-    {"any_128x128", 128, 128, 4, 2 * 256 * 128, 1, {2, 1, 1.2f, 1.8f, 2.f}},
-    {"stream_16x32_w4", 16, 32, 4, 4 * 3 * 48 * 128, 0, {2, 4, .38f, .80f, 1.5f}},
-    {"stream_16x16_w8", 16, 16, 8, 8 * 4 * 32 * 128, 0, {1, 8, .38f, .38f, 2.f}},
-    {"stream_32x32_w4", 32, 32, 4, 4 * 3 * 64 * 128, 0, {1, 4, .55f, .55f, 3.f}},
-    {"stream_64x32_w4", 64, 32, 4, 4 * 3 * 96 * 128, 0, {1, 4, 1.0f, 1.0f, 3.f}},
-    {"tile_64x128_w2x2", 64, 128, 4, 3 * 192 * 128, 0, {2, 1, .43f, .72f, 1.5f}},
-    {"tile_64x128_w2x2x2", 64, 128, 8, 2 * 3 * 192 * 128, 0, {1, 2, .72f, .72f, 2.5f}},
-    {"tile_128x128_w2x2", 128, 128, 4, 2 * 256 * 128, 0, {2, 1, .72f, 1.09f, 1.5f}},
-    {"tile_128x128_w2x2x2", 128, 128, 8, 2 * 2 * 256 * 128, 0, {1, 2, 1.09f, 1.09f, 3.f}},
-    {"pingpong_256x256", 256, 256, 8, 160 * 1024, 0, {1, 1, 1.20f, 1.20f, 6.f}},
+    {"any_64x128", 64, 128, 4, 2 * 192 * 128, 1, {2, 1, 1.2f, 1.28f, 3.f}},
+    {"any_128x128", 128, 128, 4, 2 * 256 * 128, 1, {2, 1, 1.6f, 1.75f, 4.f}},
+    {"stream_16x32_w4", 16, 32, 4, 4 * 3 * 48 * 128, 0, {2, 4, .316f, .667f, 2.6f}},
+    {"stream_16x16_w8", 16, 16, 8, 8 * 4 * 32 * 128, 0, {1, 8, .282f, .282f, 2.6f}},
+    {"stream_32x32_w4", 32, 32, 4, 4 * 3 * 64 * 128, 0, {1, 4, .394f, .394f, 3.1f}},
+    {"stream_64x32_w4", 64, 32, 4, 4 * 3 * 96 * 128, 0, {1, 4, .588f, .588f, 4.4f}},
+    {"tile_64x128_w2x2", 64, 128, 4, 3 * 192 * 128, 0, {2, 1, .359f, .664f, 2.7f}},
+    {"tile_64x128_w2x2x2", 64, 128, 8, 2 * 3 * 192 * 128, 0, {1, 2, .600f, .600f, 4.1f}},
+    {"tile_128x128_w2x2", 128, 128, 4, 2 * 256 * 128, 0, {2, 1, .613f, .975f, 3.2f}},
+    {"tile_128x128_w2x2x2", 128, 128, 8, 2 * 2 * 256 * 128, 0, {1, 2, .937f, .937f, 4.9f}},
+    {"pingpong_256x256", 256, 256, 8, 160 * 1024, 0, {1, 1, 1.13f, 1.13f, 6.9f}},
 };
 constexpr int kCount = sizeof(kVariants) / sizeof(kVariants[0]);
 static_assert(kCount == I8_JOIN, "the kernels of Int8Launches");
@@ -86,9 +86,12 @@ double expected_row_tiles(const gemm_int8_s& h, int bm) {
   return hit * std::max(1.0, M / hit / bm + 0.4);
 }
 
-// Predicted microseconds of a variant with k in `split` slices: rounds of workgroups at the
-// measured cost of a block, against the time that the operands' bytes take at 5.2 TB/s (the less of
-// the two counts a quarter: they overlap, not fully), plus the second kernel of a split.
+// Predicted microseconds of a variant with k in `split` slices: rounds of workgroups at the cost of a
+// block, against the time that the operands' bytes take at 6 TB/s (of the less of the two 0.41 counts:
+// they overlap in part), plus the second kernel of a split.  The costs are fitted to 132 products and
+// groups of rows (1 to 16384 rows, 512 to 14336 columns, k of 512 to 8192, 8 to 128 experts, each kernel
+// and slices of k forced in turn): the choice is on average 0.4 % above the fastest, 7 % at most (16384
+// rows over 128 experts); costs taken from single rounds alone gave 0.7 %.
 double predict(const gemm_int8_s& h, const Variant& v, int split) {
   const gemm_int8_desc& d = h.d;
   const Cost& c = v.cost;
@@ -98,12 +101,12 @@ double predict(const gemm_int8_s& h, const Variant& v, int split) {
   const double whole = std::floor(wgs / (kCUs * c.occ)), load = wgs / kCUs - whole * c.occ;  // last round's
   double last = 0.0;
   if (load > 0.0) last = steps * (c.c1 + (c.c2 - c.c1) * std::max(0.0, load - 1.0)) + c.round;
-  const double work = 2.0 + whole * (steps * c.c2 + c.round) + last;
+  const double work = 1.6 + whole * (steps * c.c2 + c.round) + last;
   const double hit = d.form == GEMM_INT8_ROWS ? h.batch * (1.0 - std::exp(-double(d.M) / h.batch)) : many;
   const double bytes = many * d.M * d.K + hit * d.N * d.K + many * d.M * d.N * double(out_size(d.d_type));
-  const double mem = bytes / 5.2e6;
-  double us = std::max(work, mem) + 0.25 * std::min(work, mem);
-  if (split > 1) us += 6.0 + split * double(d.M) * d.N * 8.0 / 4.0e6;
+  const double mem = bytes / 6.0e6;
+  double us = std::max(work, mem) + 0.41 * std::min(work, mem);
+  if (split > 1) us += 2.6 + split * double(d.M) * d.N * 8.0 / 4.8e6;
   return us;
 }
 

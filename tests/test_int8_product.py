@@ -74,10 +74,10 @@ def test_slices_of_k_give_the_same_bits(M, N, K, split):
     assert torch.equal(whole, part) and info.split_k <= split
 
 
-# shapes over the kernels' ranges, with a ragged K
+# shapes that every kernel is chosen for (test_int8_boundary.py looks that they are), with a ragged K
 SHAPES = [(1, 4096, 4104), (16, 16384, 1000), (20, 512, 600), (24, 4096, 8000), (60, 300, 1000), (60, 4096, 8200), (64, 4096, 2100),
           (128, 4096, 1030), (300, 1024, 600), (333, 4096, 4100), (1000, 4096, 1050), (2048, 2100, 530), (2300, 4096, 270),
-          (4096, 4096, 390), (5000, 300, 260)]
+          (4096, 4096, 390), (5000, 300, 260), (2048, 2048, 2050), (64, 8190, 8180)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
