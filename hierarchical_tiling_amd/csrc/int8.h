@@ -60,28 +60,60 @@ __device__ __forceinline__ float scaled_sum(int sum, float sa, float sb) { retur
 // 6 us: 333 x 4064 x 8192 31.9 us in place of 25.7).  With k in slices the integer sums go to the
 // slice's plane.
 // ------------------------------------------------------------------------------------------
-template <class OT, int RM, int RN, int ACT, bool HAS_C, bool EDGE, class RowOf>
-__device__ __forceinline__ void store_pieces(const SParams& p, const STile& s, const i32x4 (&acc)[RM][RN],
-                                             const float (&sa)[RM], const f32x4 (&sb)[RN], RowOf row_of, int64_t col,
-                                             int x) {
+// What a lane's outputs need besides their sums and C: scales of its rows and columns, and the bias of
+// its pieces.  Kernels with registers to spare load it before their loop, so that a short product
+// does not wait for memory once more at its end.
+template <class OT, int RM, int RN> struct Finish {
   typedef Cols<OT> CM;
-  constexpr int VO = CM::VO, NQ = RN / CM::JP, RG = RM % 2 == 0 ? 2 : 1;
-  // columns of piece q below N, and 16 bytes of it from `base` on, those past N as the last column
-  auto left = [&](int q) { return EDGE ? (int)min(p.N - col - CM::of(q * CM::JP, 0), (int64_t)VO) : VO; };
-  auto piece = [&](const void* base, int64_t row, int64_t ld, int q) {
+  static constexpr int VO = CM::VO, NQ = RN / CM::JP;
+  float sa[RM];
+  f32x4 sb[RN];
+  u32x4 bias[NQ];
+
+  // Columns of piece q (of the lane whose first column is col) below N.
+  __device__ static __forceinline__ int left(const SParams& p, int64_t col, int q) {
+    return (int)min(p.N - col - CM::of(q * CM::JP, 0), (int64_t)VO);
+  }
+  // 16 bytes of piece q of a row, zeros past N.
+  template <bool EDGE>
+  __device__ static __forceinline__ u32x4 piece(const SParams& p, const void* base, int64_t row, int64_t ld, int64_t col, int q) {
     const OT* src = (const OT*)base + row * ld + col + CM::of(q * CM::JP, 0);
-    if (!EDGE || left(q) == VO) return load16(src);
+    if (!EDGE || left(p, col, q) == VO) return load16(src);
     alignas(16) OT e[VO];
-    static_for<VO>([&](auto i) { e[i] = i < left(q) ? src[(int)i] : OT(0); });
+    static_for<VO>([&](auto i) { e[i] = i < left(p, col, q) ? src[(int)i] : OT(0); });
     u32x4 w;
     __builtin_memcpy(&w, e, 16);
     return w;
-  };
-  u32x4 bias[NQ];
-  static_for<NQ>([&](auto q) {
-    bias[q] = u32x4{0, 0, 0, 0};
-    if (p.bias) bias[q] = piece(p.bias, 0, 0, q);
-  });
+  }
+  // Split products and those without k read no scales, waves past N nothing.
+  template <class RowOf> __device__ __forceinline__ void load(const SParams& p, const STile& s, RowOf row_of, int64_t col0) {
+    const int lane = threadIdx.x & 63, x = lane & 15, c4 = lane >> 4;
+    static_for<RM>([&](auto i) { sa[i] = 0.f; });
+    static_for<RN>([&](auto j) { sb[j] = f32x4{}; });
+    static_for<NQ>([&](auto q) { bias[q] = u32x4{0, 0, 0, 0}; });
+    if (col0 >= p.N || p.split_k > 1) return;
+    const bool whole = col0 + 16 * RN <= p.N;
+    if (p.K > 0) {
+      static_for<RN>([&](auto j) {
+        const int64_t n = col0 + CM::of(j, c4);
+        if (whole) __builtin_memcpy(&sb[j], s.b_scale + n, 16);
+        else static_for<4>([&](auto r) { sb[j][(int)r] = s.b_scale[min(n + r, p.N - 1)]; });
+      });
+      static_for<RM>([&](auto i) { sa[i] = s.a_scale[min(row_of(i, x), s.M - 1)]; });
+    }
+    if (p.bias) {
+      const int64_t col = col0 + CM::of(0, c4);
+      static_for<NQ>([&](auto q) { bias[q] = whole ? piece<false>(p, p.bias, 0, 0, col, q) : piece<true>(p, p.bias, 0, 0, col, q); });
+    }
+  }
+};
+
+template <class OT, int RM, int RN, int ACT, bool HAS_C, bool EDGE, class RowOf>
+__device__ __forceinline__ void store_pieces(const SParams& p, const STile& s, const i32x4 (&acc)[RM][RN],
+                                             const Finish<OT, RM, RN>& f, RowOf row_of, int64_t col, int x) {
+  typedef Finish<OT, RM, RN> F;
+  typedef Cols<OT> CM;
+  constexpr int VO = F::VO, NQ = F::NQ, RG = RM % 2 == 0 ? 2 : 1;
   // RG row blocks at a time, whose C is loaded before they are stored: D may be C, and more in hand at
   // once would not fit the registers
   static_for<RM / RG>([&](auto i0) {
@@ -91,7 +123,7 @@ __device__ __forceinline__ void store_pieces(const SParams& p, const STile& s, c
       static_for<NQ>([&](auto q) {
         c[h][q] = u32x4{0, 0, 0, 0};
         if constexpr (HAS_C)
-          if (row < s.M) c[h][q] = piece(s.C, row, p.ldc, q);
+          if (row < s.M) c[h][q] = F::template piece<EDGE>(p, s.C, row, p.ldc, col, q);
       });
     });
     static_for<RG>([&](auto h) {
@@ -103,17 +135,18 @@ __device__ __forceinline__ void store_pieces(const SParams& p, const STile& s, c
           alignas(16) OT o[VO];
           static_for<VO>([&](auto e) {
             constexpr int j = q * CM::JP + e / 4, r = e % 4;
-            float y = scaled_sum(acc[i][j][r], sa[i], sb[j][r]) * p.alpha;
+            float y = scaled_sum(acc[i][j][r], f.sa[i], f.sb[j][r]) * p.alpha;
             if constexpr (HAS_C) y += p.beta * SOut<OT>::load(&c[h][q], e);
-            y += SOut<OT>::load(&bias[q], e);
+            y += SOut<OT>::load(&f.bias[q], e);
             o[e] = SOut<OT>::bits(ACT < 0 ? activate(p.act, y) : ACT == 1 ? relu(y) : ACT == 2 ? gelu(y) : ACT == 3 ? silu(y) : y);
           });
           OT* to = d + CM::of(q * CM::JP, 0);
-          if (!EDGE || left(q) == VO) {
+          const int left = EDGE ? F::left(p, col, q) : VO;
+          if (!EDGE || left == VO) {
             __builtin_memcpy(to, o, 16);
           } else {
             static_for<VO>([&](auto e) {
-              if (e < left(q)) to[(int)e] = o[e];
+              if (e < left) to[(int)e] = o[e];
             });
           }
         });
@@ -125,12 +158,11 @@ __device__ __forceinline__ void store_pieces(const SParams& p, const STile& s, c
 // col0: the wave's first column (at or past N for a wave that stores nothing); row_of(i, x): the row
 // of row block i in lane x = lane % 16.
 template <class OT, int RM, int RN, class RowOf>
-__device__ __forceinline__ void store_sums(const SParams& p, const STile& s, const i32x4 (&acc)[RM][RN], RowOf row_of,
-                                           int64_t col0) {
+__device__ __forceinline__ void store_sums(const SParams& p, const STile& s, const i32x4 (&acc)[RM][RN],
+                                           const Finish<OT, RM, RN>& f, RowOf row_of, int64_t col0) {
   typedef Cols<OT> CM;
   const int lane = threadIdx.x & 63, x = lane & 15, c4 = lane >> 4;
   if (col0 >= p.N) return;
-  const bool whole = col0 + 16 * RN <= p.N;
   if (p.split_k > 1) {
     int* plane = reinterpret_cast<int*>(p.workspace) + (int64_t)blockIdx.y * p.M * p.N + col0;
     static_for<RM>([&](auto i) {
@@ -148,40 +180,27 @@ __device__ __forceinline__ void store_sums(const SParams& p, const STile& s, con
     });
     return;
   }
-  float sa[RM];
-  f32x4 sb[RN];
-  static_for<RM>([&](auto i) { sa[i] = 0.f; });
-  static_for<RN>([&](auto j) { sb[j] = f32x4{}; });
-  if (p.K > 0) {                // a product without k reads no scales
-    static_for<RN>([&](auto j) {
-      const int64_t n = col0 + CM::of(j, c4);
-      if (whole) __builtin_memcpy(&sb[j], s.b_scale + n, 16);
-      else static_for<4>([&](auto r) { sb[j][(int)r] = s.b_scale[min(n + r, p.N - 1)]; });
-    });
-    static_for<RM>([&](auto i) { sa[i] = s.a_scale[min(row_of(i, x), s.M - 1)]; });
-  }
   const int64_t col = col0 + CM::of(0, c4);
   auto go = [&](auto act, auto edge) {
     constexpr int A = decltype(act)::value;
     constexpr bool E = decltype(edge)::value;
-    if (s.C) store_pieces<OT, RM, RN, A, true, E>(p, s, acc, sa, sb, row_of, col, x);
-    else store_pieces<OT, RM, RN, A, false, E>(p, s, acc, sa, sb, row_of, col, x);
+    if (s.C) store_pieces<OT, RM, RN, A, true, E>(p, s, acc, f, row_of, col, x);
+    else store_pieces<OT, RM, RN, A, false, E>(p, s, acc, f, row_of, col, x);
   };
-  if (!whole) go(std::integral_constant<int, -1>{}, std::true_type{});
+  if (col0 + 16 * RN > p.N) go(std::integral_constant<int, -1>{}, std::true_type{});
   else if (p.act == 0) go(std::integral_constant<int, 0>{}, std::false_type{});
   else if (p.act == 3) go(std::integral_constant<int, 3>{}, std::false_type{});
   else if (p.act == 2) go(std::integral_constant<int, 2>{}, std::false_type{});
   else go(std::integral_constant<int, 1>{}, std::false_type{});
 }
 
-// One output from its sum.
+// One output from its sum, its scales and its bias.
 template <class OT>
-__device__ __forceinline__ void finish_int(const SParams& p, const STile& s, int64_t row, int64_t col, int sum) {
-  float v = p.K > 0 ? scaled_sum(sum, s.a_scale[row], s.b_scale[col]) : 0.f;
-  v *= p.alpha;
+__device__ __forceinline__ void finish_int(const SParams& p, const STile& s, int64_t row, int64_t col, int sum, float sa,
+                                           float sb, float bias) {
+  float v = scaled_sum(sum, sa, sb) * p.alpha;
   if (s.C) v += p.beta * SOut<OT>::load(s.C, row * p.ldc + col);
-  if (p.bias) v += SOut<OT>::load(p.bias, col);
-  ((OT*)s.D)[row * p.ldd + col] = SOut<OT>::bits(activate(p.act, v));
+  ((OT*)s.D)[row * p.ldd + col] = SOut<OT>::bits(activate(p.act, v + bias));
 }
 
 // Spans of a tile's rows for the range checks: up to the end of the chunk that K ends in.
@@ -261,6 +280,9 @@ __global__ __launch_bounds__(256, OCC) void i8_any(const SParams p) {
   i32x4 acc[RM][RN];
   static_for<RM>([&](auto i) { static_for<RN>([&](auto j) { acc[i][j] = i32x4{}; }); });
   if (nk > 0) load(0);
+  auto row_of = [&](int i, int r) { return s.m0 + wm * TM + r * RM + i; };
+  Finish<OT, RM, RN> finish;
+  finish.load(p, s, row_of, s.n0 + wn * TN);
   for (int t = 0; t < nk; ++t) {
     u32x4* st = lds + (t & 1) * ROWS * 8;
     static_for<NCH>([&](auto i) { st[swizzled_slot<8>((tid >> 3) + i * 32, c)] = w[i]; });
@@ -273,7 +295,7 @@ __global__ __launch_bounds__(256, OCC) void i8_any(const SParams p) {
       static_for<RM>([&](auto i) { static_for<RN>([&](auto j) { mma_i8(acc[i][j], fb[j], fa[i]); }); });
     });
   }
-  store_sums<OT, RM, RN>(p, s, acc, [&](int i, int r) { return s.m0 + wm * TM + r * RM + i; }, s.n0 + wn * TN);
+  store_sums<OT, RM, RN>(p, s, acc, finish, row_of, s.n0 + wn * TN);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -357,6 +379,10 @@ __global__ __launch_bounds__(KH * WM * WN * 64, OCC) void i8_tile(const SParams 
     });
   };
 
+  auto row_of = [&](int i, int r) { return s.m0 + wm * TM + r * RM + i; };
+  const int64_t col0 = half == 0 ? s.n0 + wn * TN : p.N;
+  Finish<OT, RM, RN> finish;
+  finish.load(p, s, row_of, col0);
   if (nk > 0) {
     static_for<ST - 1>([&](auto q) { dma(q, q); });
     int stage = 0;
@@ -381,8 +407,7 @@ __global__ __launch_bounds__(KH * WM * WN * 64, OCC) void i8_tile(const SParams 
     __syncthreads();
     if (half == 0) static_for<RM>([&](auto i) { static_for<RN>([&](auto j) { acc[i][j] += sums[(i * RN + j) * 64]; }); });
   }
-  store_sums<OT, RM, RN>(p, s, acc, [&](int i, int r) { return s.m0 + wm * TM + r * RM + i; },
-                         half == 0 ? s.n0 + wn * TN : p.N);
+  store_sums<OT, RM, RN>(p, s, acc, finish, row_of, col0);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -421,6 +446,18 @@ __global__ __launch_bounds__(WK * 64, OCC) void i8_stream(const SParams p) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(IS_A ? ra : rb, (lds_void_t*)(&ring[wave][slot][c * 64]), 16, o, sk, 0, 0);
     });
   };
+  // scales and bias of the outputs that this thread joins: before the loop, as they would otherwise be
+  // one more wait for memory in a kernel of a few microseconds
+  constexpr int NO = (BM * BN + NT - 1) / NT;
+  float sa[NO], sb[NO], bias[NO];
+  static_for<NO>([&](auto o) {
+    const int q = min(tid + o * NT, BM * BN - 1);
+    const int64_t m = min(s.m0 + q / BN, s.M - 1), n = min(s.n0 + q % BN, p.N - 1);
+    const bool scaled = p.K > 0 && p.split_k <= 1;
+    sa[o] = scaled ? s.a_scale[m] : 0.f;
+    sb[o] = scaled ? s.b_scale[n] : 0.f;
+    bias[o] = p.bias ? SOut<OT>::load(p.bias, n) : 0.f;
+  });
   i32x4 acc[RM][NBW];
   static_for<RM>([&](auto i) { static_for<NBW>([&](auto j) { acc[i][j] = i32x4{}; }); });
   auto compute = [&](auto slot, bool last) {
@@ -457,16 +494,17 @@ __global__ __launch_bounds__(WK * 64, OCC) void i8_stream(const SParams p) {
     });
   });
   __syncthreads();
-  for (int q = tid; q < BM * BN; q += NT) {
-    const int row = q / BN, c = q % BN;
+  static_for<NO>([&](auto o) {
+    const int q = tid + o * NT, row = q / BN, c = q % BN;
     const int64_t m = s.m0 + row, n = s.n0 + c;
-    if (m >= s.M || n >= p.N) continue;
-    int sum = 0;
+    if (q < BM * BN && m < s.M && n < p.N) {
+      int sum = 0;
 #pragma unroll
-    for (int w = 0; w < WK; ++w) sum += part[(w * BM + row) * PITCH + c];
-    if (p.split_k > 1) reinterpret_cast<int*>(p.workspace)[((int64_t)blockIdx.y * p.M + m) * p.N + n] = sum;
-    else finish_int<OT>(p, s, m, n, sum);
-  }
+      for (int w = 0; w < WK; ++w) sum += part[(w * BM + row) * PITCH + c];
+      if (p.split_k > 1) reinterpret_cast<int*>(p.workspace)[((int64_t)blockIdx.y * p.M + m) * p.N + n] = sum;
+      else finish_int<OT>(p, s, m, n, sum, sa[o], sb[o], bias[o]);
+    }
+  });
 }
 
 // ------------------------------------------------------------------------------------------
@@ -567,17 +605,18 @@ __global__ __launch_bounds__(512, 1) void i8_pp(const SParams p) {
         static_for<2>([&](auto u) { static_for<RM>([&](auto i) { fa[u][i] = keep_bytes(fa[u][i], cut - (c4 + 4 * u) * 16); }); });
       wait_counts<8, true>();
       phase_end();
-      __builtin_amdgcn_s_setprio(1);     // the computing wave before the one that reads
       static_for<2>([&](auto u) {
         static_for<RM>([&](auto i) { static_for<RN>([&](auto j) { mma_i8(acc[i][j], fb[u][j], fa[u][i]); }); });
       });
-      __builtin_amdgcn_s_setprio(0);
       phase_end();
     }
     if (g == 0) phase_end();
     wait_counts<0, true>();     // zero blocks issued past the end
   }
-  store_sums<OT, RM, RN>(p, s, acc, [&](int i, int r) { return s.m0 + g * 128 + r * 8 + i; }, s.n0 + wq * 64);
+  auto row_of = [&](int i, int r) { return s.m0 + g * 128 + r * 8 + i; };
+  Finish<OT, RM, RN> finish;
+  finish.load(p, s, row_of, s.n0 + wq * 64);
+  store_sums<OT, RM, RN>(p, s, acc, finish, row_of, s.n0 + wq * 64);
 }
 
 // The planes of a split k, added, and the epilogue.
@@ -594,7 +633,7 @@ __global__ __launch_bounds__(256) void i8_join(const SParams p) {
     const int64_t row = e / p.N, col = e - row * p.N;
     int sum = 0;
     for (int q = 0; q < p.split_k; ++q) sum += planes[q * MN + e];
-    finish_int<OT>(p, s, row, col, sum);
+    finish_int<OT>(p, s, row, col, sum, s.a_scale[row], s.b_scale[col], p.bias ? SOut<OT>::load(p.bias, col) : 0.f);
   }
 }
 

@@ -3,7 +3,8 @@
 //   t = max(largest |x|, 127 * 2^-126),  scale = t / 127,  q = clamp(rint(x * (127 / t)), -127, 127)
 //
 // A row is read once and kept in registers between the maximum and the conversion.  Bound by
-// memory.
+// memory: 16384 x 8192 bf16 66 us, 6.1 TB/s (a copy reaches 4.7, a kernel that only reads 6.3).  Codes
+// are stored past the caches (16384 x 8192 75 -> 70 us, 20000 x 2048 26 -> 20; small ones are alike).
 #include <algorithm>
 
 #include "../../include/htint8.h"
@@ -40,12 +41,18 @@ template <> struct RowType<DT_F16> {
 
 // Columns c .. c + 7 of a row as fp32, zero past its end.  The loads of a chunk that a row ends in have
 // clamped addresses; 16-byte loads go at any alignment.
-template <int XT> __device__ __forceinline__ void row8(const void* row, int c, int cols, float (&v)[8]) {
+typedef u32x4 piece_t __attribute__((aligned(2)));
+typedef uint64_t codes_t __attribute__((aligned(1)));
+template <int XT, bool STREAM> __device__ __forceinline__ void row8(const void* row, int c, int cols, float (&v)[8]) {
   typedef typename RowType<XT>::T T;
   const T* src = (const T*)row;
   if (c + 8 <= cols) {
     alignas(16) T e[8];
-    __builtin_memcpy(e, src + c, sizeof(e));
+    const piece_t* from = reinterpret_cast<const piece_t*>(src + c);
+    static_for<(int)sizeof(e) / 16>([&](auto h) {
+      const u32x4 w = STREAM ? (u32x4)__builtin_nontemporal_load(from + h) : (u32x4)from[(int)h];
+      __builtin_memcpy(reinterpret_cast<char*>(e) + 16 * h, &w, 16);
+    });
     static_for<8>([&](auto i) { v[i] = RowType<XT>::up(e[i]); });
   } else if (c < cols) {
     T e[8];
@@ -56,12 +63,12 @@ template <int XT> __device__ __forceinline__ void row8(const void* row, int c, i
   }
 }
 
-template <int XT, bool GATE>
+template <int XT, bool GATE, bool STREAM>
 __device__ __forceinline__ void values8(const QRParams& p, const void* x, const void* gate, int c, float (&v)[8]) {
-  row8<XT>(x, c, p.cols, v);
+  row8<XT, STREAM>(x, c, p.cols, v);
   if constexpr (GATE) {
     float g[8];
-    row8<XT>(gate, c, p.cols, g);
+    row8<XT, STREAM>(gate, c, p.cols, g);
     static_for<8>([&](auto i) { v[i] = c + i < p.cols ? activate(p.act, g[i]) * v[i] : 0.f; });
   }
 }
@@ -103,7 +110,7 @@ __device__ __forceinline__ void store8(const QRParams& p, u8* q, int c, const fl
   uint64_t w = (uint64_t)codes4(v[4], v[5], v[6], v[7], inverse) << 32 | codes4(v[0], v[1], v[2], v[3], inverse);
   if (bad) w = 0;
   if (c + 8 <= p.q_cols) {
-    __builtin_memcpy(q + c, &w, 8);
+    __builtin_nontemporal_store(w, reinterpret_cast<codes_t*>(q + c));
   } else {
     const int n = p.q_cols - c;
 #pragma unroll 1
@@ -113,7 +120,7 @@ __device__ __forceinline__ void store8(const QRParams& p, u8* q, int c, const fl
 
 // TPR threads take a row, NC pieces of 8 columns each (TPR * 8 columns apart); rows of more than
 // TPR * NC * 8 columns (LONG) are read a second time for the conversion.
-template <int XT, bool GATE, int TPR, int NC, bool LONG>
+template <int XT, bool GATE, bool STREAM, int TPR, int NC, bool LONG>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_to_int8(const QRParams p) {
   constexpr int PER = TPR < 256 ? 256 / TPR : 1, NW = TPR / 64;
   __shared__ u32 tops[NW > 1 ? NW : 1];
@@ -134,12 +141,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_to_int8(const QRPa
   u32 top = 0;
   static_for<NC>([&](auto k) { static_for<8>([&](auto i) { v[k][i] = 0.f; }); });
   if (from >= 0) {
-    static_for<NC>([&](auto k) { values8<XT, GATE>(p, x, gate, (k * TPR + tid) * 8, v[k]); });
+    static_for<NC>([&](auto k) { values8<XT, GATE, STREAM>(p, x, gate, (k * TPR + tid) * 8, v[k]); });
     static_for<NC>([&](auto k) { top = magnitude(v[k], top); });
     if constexpr (LONG) {
       for (int c = (NC * TPR + tid) * 8; c < p.cols; c += TPR * 8) {
         float w[8];
-        values8<XT, GATE>(p, x, gate, c, w);
+        values8<XT, GATE, STREAM>(p, x, gate, c, w);
         top = magnitude(w, top);
       }
     }
@@ -162,7 +169,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_to_int8(const QRPa
     for (int c = (NC * TPR + tid) * 8; c < p.q_cols; c += TPR * 8) {
       float w[8];
       static_for<8>([&](auto i) { w[i] = 0.f; });
-      if (from >= 0) values8<XT, GATE>(p, x, gate, c, w);
+      if (from >= 0) values8<XT, GATE, STREAM>(p, x, gate, c, w);
       store8(p, q, c, w, inverse, bad);
     }
   }
@@ -175,19 +182,33 @@ dim3 grid_of(int64_t blocks) {
   return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
 }
 
-template <int XT, bool GATE> hipError_t launch(const QRParams& p, hipStream_t s) {
+// Threads for each row: a wave for short rows, a workgroup for longer ones, and more of them while there
+// are too few rows to fill the card (480 x 2048 with 256 threads a row 2.8 us, a wave 3.4, gated 3.6 and
+// 6.7; 4096 x 2048 6.5 and 6.0; 1 x 8192 with 1024 threads 2.6, 256 3.1; 2000 x 8192 10.8 and 9.4).
+template <int XT, bool GATE, bool STREAM> hipError_t launch(const QRParams& p, hipStream_t s) {
   auto go = [&](auto kernel, int tpr) {
     const int per = tpr < 256 ? 256 / tpr : 1;
     hipLaunchKernelGGL(kernel, grid_of((p.rows + per - 1) / per), dim3(tpr < 256 ? 256 : tpr), 0, s, p);
   };
   const int n = p.q_cols;
-  if (n <= 512) go(rows_to_int8<XT, GATE, 64, 1, false>, 64);
-  else if (n <= 2048) go(rows_to_int8<XT, GATE, 64, 4, false>, 64);
-  else if (n <= 4096) go(rows_to_int8<XT, GATE, 256, 2, false>, 256);
-  else if (n <= 8192) go(rows_to_int8<XT, GATE, 256, 4, false>, 256);
-  else if (n <= 32768) go(rows_to_int8<XT, GATE, 1024, 4, false>, 1024);
-  else go(rows_to_int8<XT, GATE, 1024, 4, true>, 1024);
+  if (n <= 512) go(rows_to_int8<XT, GATE, STREAM, 64, 1, false>, 64);
+  else if (n <= 2048 && p.rows <= 1024) go(rows_to_int8<XT, GATE, STREAM, 256, 1, false>, 256);
+  else if (n <= 1024) go(rows_to_int8<XT, GATE, STREAM, 64, 2, false>, 64);
+  else if (n <= 2048) go(rows_to_int8<XT, GATE, STREAM, 64, 4, false>, 64);
+  else if (n <= 4096) go(rows_to_int8<XT, GATE, STREAM, 256, 2, false>, 256);
+  else if (n <= 8192 && p.rows <= 256) go(rows_to_int8<XT, GATE, STREAM, 1024, 1, false>, 1024);
+  else if (n <= 8192) go(rows_to_int8<XT, GATE, STREAM, 256, 4, false>, 256);
+  else if (n <= 32768) go(rows_to_int8<XT, GATE, STREAM, 1024, 4, false>, 1024);
+  else go(rows_to_int8<XT, GATE, STREAM, 1024, 4, true>, 1024);
   return hipGetLastError();
+}
+// An input that no cache holds is read past the caches: 16384 x 8192 bf16 (268 MB) 70 -> 66 us, 16384 x
+// 4096 34.7 -> 33.3; 20000 x 2048 (82 MB, three in turn) 20.3 -> 22.6.
+constexpr int64_t kStreamBytes = int64_t(1) << 27;
+template <int XT> hipError_t launch_type(const QRParams& p, hipStream_t s) {
+  const bool big = p.x_rows * p.cols >= kStreamBytes / (XT == DT_F32 ? 4 : 2);
+  if (p.gate) return big ? launch<XT, true, true>(p, s) : launch<XT, true, false>(p, s);
+  return big ? launch<XT, false, true>(p, s) : launch<XT, false, false>(p, s);
 }
 
 bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -231,9 +252,8 @@ extern "C" int quant_rows(const quant_rows_args* a, void* stream) {
   p.index_div = a->index_div;
   p.act = a->act;
   hipStream_t s = (hipStream_t)stream;
-  const bool g = a->gate != nullptr;
-  const hipError_t err = a->x_type == GEMM_F32   ? (g ? launch<DT_F32, true>(p, s) : launch<DT_F32, false>(p, s))
-                         : a->x_type == GEMM_F16 ? (g ? launch<DT_F16, true>(p, s) : launch<DT_F16, false>(p, s))
-                                                 : (g ? launch<DT_BF16, true>(p, s) : launch<DT_BF16, false>(p, s));
+  const hipError_t err = a->x_type == GEMM_F32   ? launch_type<DT_F32>(p, s)
+                         : a->x_type == GEMM_F16 ? launch_type<DT_F16>(p, s)
+                                                 : launch_type<DT_BF16>(p, s);
   return err == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
