@@ -9,7 +9,7 @@ import struct
 
 from . import htgemm
 from .htgemm import ACTS, DTYPES, GEMM_ERR_INVALID_ARG, GemmError, _check
-from .htscaled import _bytes, _elsewhere, _here, _padded, pitch, type_code
+from .htscaled import _bytes, _here, _padded, pitch, type_code
 
 FORMS = {"single": 0, "batch": 1, "rows": 2}
 _i32, _i64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
@@ -179,7 +179,8 @@ class Int8Gemm:
         if workspace is None:
             workspace = 0
         elif workspace.__class__ is not int:
-            if workspace.get_device() != dev or (self._room and _bytes(workspace) < self._room):
+            if workspace.get_device() != dev or (self._room and not (
+                    (workspace.numel() >= self._room and workspace.is_contiguous()) or _bytes(workspace) >= self._room)):
                 raise GemmError(GEMM_ERR_INVALID_ARG, "gemm_int8_run")
             workspace = workspace.data_ptr()
         rc = _lib.gemm_int8_run(self.handle, _ARGS.pack(A, a_scale, B, b_scale, C, D, bias, offsets, alpha, beta, workspace),
@@ -204,13 +205,13 @@ assert _QUANT.size == ctypes.sizeof(quant_rows_args)
 
 
 def _types():
-    global _i8, _i32t
+    global _i8, _i32t, _f32t
     import torch
-    _i32t = torch.int32      # (first: another thread looks at the other)
-    _i8 = torch.int8
+    _i32t, _f32t = torch.int32, torch.float32
+    _i8 = torch.int8      # (last: another thread looks at it)
 
 
-_i8 = _i32t = None
+_i8 = _i32t = _f32t = None
 
 
 def quantize(x, q, scale, gate=None, act=None, row_index=None, index_div=1, pad=False, stream=None):
@@ -222,31 +223,28 @@ def quantize(x, q, scale, gate=None, act=None, row_index=None, index_div=1, pad=
     the padding does, and tensors on another device than the current one raise GemmError."""
     if _i8 is None:
         _types()
-    ok = x.dim() == 2 and q.dim() == 2
-    if ok:
-        x_rows, cols = x.shape
-        step = pitch(x, x_rows, cols)
-        rows, index = x_rows, 0
-        if row_index is not None:
-            rows, index = row_index.numel(), row_index.data_ptr()
-            ok = row_index.dtype is _i32t and row_index.is_contiguous()
-        to = pitch(q, rows, cols)
-        ok = (ok and step >= 0 and to >= 0 and q.shape == (rows, cols) and q.dtype is _i8 and
-              scale.numel() == rows and scale.is_contiguous() and type_code(scale) == 0)
-        if ok and pad:
-            ok = _padded(q, (0, to), rows, cols)
-        ldg = at = code = 0
-        if gate is not None:
-            ok = ok and gate.shape == x.shape and gate.dtype is x.dtype
-            if ok:
-                ldg, at, code = pitch(gate, x_rows, cols), gate.data_ptr(), ACTS["silu" if act is None else act]
-                ok = ldg >= 0
-        elif act is not None:
-            ok = False
-    if not ok:
-        raise GemmError(GEMM_ERR_INVALID_ARG, "quantize")
     dev, stream = _here(stream)
-    if _elsewhere(dev, x, q, scale, gate, row_index):
+    if x.dim() != 2:
+        raise GemmError(GEMM_ERR_INVALID_ARG, "quantize")
+    x_rows, cols = x.shape
+    rows, index, ldg, at, code = x_rows, 0, 0, 0, 0
+    ok = gate is not None or act is None
+    if row_index is not None:
+        rows, index = row_index.numel(), row_index.data_ptr()
+        ok = ok and row_index.dtype is _i32t and row_index.is_contiguous() and row_index.get_device() == dev
+    if gate is not None:
+        ok = ok and gate.shape == x.shape and gate.dtype is x.dtype and gate.get_device() == dev
+        if ok:
+            ldg, at, code = pitch(gate, x_rows, cols), gate.data_ptr(), ACTS["silu" if act is None else act]
+            ok = ldg >= 0
+    ok = (ok and q.dtype is _i8 and scale.dtype is _f32t and q.shape == (rows, cols) and scale.numel() == rows and
+          scale.is_contiguous() and x.get_device() == dev and q.get_device() == dev and scale.get_device() == dev)
+    if ok:
+        step = cols if x.is_contiguous() else pitch(x, x_rows, cols)
+        # (of one padded row the stride says how far its padding may go)
+        to = cols if not pad and q.is_contiguous() else pitch(q, rows, cols)
+        ok = step >= 0 and to >= 0 and (not pad or _padded(q, (0, to), rows, cols))
+    if not ok:
         raise GemmError(GEMM_ERR_INVALID_ARG, "quantize")
     rc = (_lib or lib()).quant_rows(_QUANT.pack(x.data_ptr(), at, type_code(x), code, rows, cols, step, ldg, index,
                                                 x_rows, index_div, pad, q.data_ptr(), to, scale.data_ptr()), stream)

@@ -199,25 +199,23 @@ def balance_grad(logits, counts, topk, live, d_loss, d_logits, mask=None, coef=1
         raise GemmError(rc, "balance_grad")
 
 
-def _matrix(t, rows, cols, dtype):
-    """Row stride of a rows x cols tensor of a type with contiguous rows; -1 of any other."""
-    return pitch(t, rows, cols) if t.dtype is dtype and t.shape == (rows, cols) else -1
-
-
 def gather(x, order, slot, y, stream=None):
     """route_gather: the tokens x (tokens, cols) to their experts' rows y (rows, cols), by route()'s
     order (rows) and slot (tokens, topk); rows of no assignment become zeros.  The gradient with
     respect to x is combine() of y's gradient without weights."""
     if _i32t is None:
         _types()
+    dev, stream = _here(stream)
     if x.dim() != 2 or slot.dim() != 2:
         raise _bad("gather")
-    (tokens, cols), topk, rows = x.shape, slot.shape[1], order.numel()
-    ldx, ldy = pitch(x, tokens, cols), _matrix(y, rows, cols, x.dtype)
-    if ldx < 0 or ldy < 0 or not _is(order, _i32t, rows) or not _is(slot, _i32t, tokens * topk):
+    (tokens, cols), (n, topk), rows = x.shape, slot.shape, order.numel()
+    if (order.dtype is not _i32t or slot.dtype is not _i32t or n != tokens or y.dtype is not x.dtype or
+            y.shape != (rows, cols) or not order.is_contiguous() or not slot.is_contiguous() or
+            x.get_device() != dev or order.get_device() != dev or slot.get_device() != dev or y.get_device() != dev):
         raise _bad("gather")
-    dev, stream = _here(stream)
-    if _elsewhere(dev, x, order, slot, y):
+    ldx = cols if x.is_contiguous() else pitch(x, tokens, cols)
+    ldy = cols if y.is_contiguous() else pitch(y, rows, cols)
+    if ldx < 0 or ldy < 0:
         raise _bad("gather")
     rc = (_lib or lib()).route_gather(_GATHER.pack(x.data_ptr(), type_code(x), topk, tokens, cols, ldx, order.data_ptr(),
                                                    slot.data_ptr(), y.data_ptr(), rows, ldy), stream)
@@ -231,21 +229,25 @@ def combine(y, slot, out, weights=None, add=None, stream=None):
     be add."""
     if _i32t is None:
         _types()
+    dev, stream = _here(stream)
     if y.dim() != 2 or slot.dim() != 2:
         raise _bad("combine")
     (rows, cols), (tokens, topk) = y.shape, slot.shape
-    ldy, ld_out = pitch(y, rows, cols), _matrix(out, tokens, cols, y.dtype)
+    if (slot.dtype is not _i32t or not slot.is_contiguous() or out.dtype is not y.dtype or out.shape != (tokens, cols) or
+            y.get_device() != dev or slot.get_device() != dev or out.get_device() != dev):
+        raise _bad("combine")
+    ldy = cols if y.is_contiguous() else pitch(y, rows, cols)
+    ld_out = cols if out.is_contiguous() else pitch(out, tokens, cols)
     ld_add = at = w = w_type = 0
     if add is not None:
-        ld_add, at = _matrix(add, tokens, cols, y.dtype), add.data_ptr()
+        if add.dtype is not y.dtype or add.shape != (tokens, cols) or add.get_device() != dev:
+            raise _bad("combine")
+        ld_add, at = pitch(add, tokens, cols), add.data_ptr()
     if weights is not None:
-        if weights.shape != slot.shape or not weights.is_contiguous():
+        if weights.shape != (tokens, topk) or not weights.is_contiguous() or weights.get_device() != dev:
             raise _bad("combine")
         w, w_type = weights.data_ptr(), type_code(weights)
-    if ldy < 0 or ld_out < 0 or ld_add < 0 or not _is(slot, _i32t, tokens * topk):
-        raise _bad("combine")
-    dev, stream = _here(stream)
-    if _elsewhere(dev, y, slot, out, weights, add):
+    if ldy < 0 or ld_out < 0 or ld_add < 0:
         raise _bad("combine")
     rc = (_lib or lib()).route_combine(_COMBINE.pack(y.data_ptr(), type_code(y), w_type, rows, cols, ldy, slot.data_ptr(), w,
                                                      at, ld_add, out.data_ptr(), ld_out, tokens, topk), stream)
@@ -259,25 +261,33 @@ def combine_grad(d_out, y, order, slot, weights, d_y=None, d_weights=None, strea
     d_weights only, and may be None without it."""
     if _i32t is None:
         _types()
+    dev, stream = _here(stream)
     if d_out.dim() != 2 or slot.dim() != 2 or (d_y is None and d_weights is None) or (y is None and d_weights is not None):
         raise _bad("combine_grad")
-    (tokens, cols), topk, rows = d_out.shape, slot.shape[1], order.numel()
-    ld_out, ldy, ld_dy = pitch(d_out, tokens, cols), 0, 0
-    if y is not None:
-        ldy = _matrix(y, rows, cols, d_out.dtype)
-    if d_y is not None:
-        ld_dy = _matrix(d_y, rows, cols, d_out.dtype)
-    if (ld_out < 0 or ldy < 0 or ld_dy < 0 or not _is(order, _i32t, rows) or not _is(slot, _i32t, tokens * topk) or
-            weights.shape != slot.shape or not weights.is_contiguous() or
-            (d_weights is not None and not (_is(d_weights, weights.dtype, tokens * topk)))):
+    (tokens, cols), (n, topk), rows, dtype = d_out.shape, slot.shape, order.numel(), d_out.dtype
+    if (order.dtype is not _i32t or slot.dtype is not _i32t or n != tokens or not order.is_contiguous() or
+            not slot.is_contiguous() or weights.shape != (tokens, topk) or not weights.is_contiguous() or
+            d_out.get_device() != dev or order.get_device() != dev or slot.get_device() != dev or weights.get_device() != dev):
         raise _bad("combine_grad")
-    dev, stream = _here(stream)
-    if _elsewhere(dev, d_out, y, order, slot, weights, d_y, d_weights):
+    ld_out = cols if d_out.is_contiguous() else pitch(d_out, tokens, cols)
+    ldy = ld_dy = at = to = d_w = 0
+    if y is not None:
+        if y.dtype is not dtype or y.shape != (rows, cols) or y.get_device() != dev:
+            raise _bad("combine_grad")
+        ldy, at = cols if y.is_contiguous() else pitch(y, rows, cols), y.data_ptr()
+    if d_y is not None:
+        if d_y.dtype is not dtype or d_y.shape != (rows, cols) or d_y.get_device() != dev:
+            raise _bad("combine_grad")
+        ld_dy, to = cols if d_y.is_contiguous() else pitch(d_y, rows, cols), d_y.data_ptr()
+    if d_weights is not None:
+        if (d_weights.dtype is not weights.dtype or d_weights.shape != (tokens, topk) or not d_weights.is_contiguous() or
+                d_weights.get_device() != dev):
+            raise _bad("combine_grad")
+        d_w = d_weights.data_ptr()
+    if ld_out < 0 or ldy < 0 or ld_dy < 0:
         raise _bad("combine_grad")
     rc = (_lib or lib()).route_combine_grad(
-        _COMBINE_GRAD.pack(d_out.data_ptr(), 0 if y is None else y.data_ptr(), type_code(d_out), type_code(weights), tokens,
-                           rows, cols, ld_out, ldy, order.data_ptr(), slot.data_ptr(), weights.data_ptr(),
-                           0 if d_y is None else d_y.data_ptr(), ld_dy, 0 if d_weights is None else d_weights.data_ptr(),
-                           topk), stream)
+        _COMBINE_GRAD.pack(d_out.data_ptr(), at, type_code(d_out), type_code(weights), tokens, rows, cols, ld_out, ldy,
+                           order.data_ptr(), slot.data_ptr(), weights.data_ptr(), to, ld_dy, d_w, topk), stream)
     if rc:
         raise GemmError(rc, "route_combine_grad")
