@@ -571,6 +571,8 @@ __global__ __launch_bounds__(512, 1) void i8_pp(const SParams p) {
                                                in_k ? o + (uint32_t)(cols * p.ldb) : kOobOffset, t < nk ? (int)k : 0, 0, 0);
     });
   };
+  // a group whose rows all lie past M (half of a group's last tiles) leaves the SIMDs to the other
+  const bool works = s.m0 + g * 128 < s.M;
   u32x4 fa[2][RM], fb[2][RN];
   auto read_frags = [&](int t) {
     static_for<2>([&](auto u) {
@@ -598,16 +600,17 @@ __global__ __launch_bounds__(512, 1) void i8_pp(const SParams p) {
     barrier_nofence();
     if (g == 1) phase_end();
     for (int v = 0; v < nk; ++v) {
-      read_frags(v);
+      if (works) read_frags(v);
       dma_a(1 - g, v + 1 + g);
       dma_b(v + 2);
       if (v == nk - 1 && cut)
         static_for<2>([&](auto u) { static_for<RM>([&](auto i) { fa[u][i] = keep_bytes(fa[u][i], cut - (c4 + 4 * u) * 16); }); });
       wait_counts<8, true>();
       phase_end();
-      static_for<2>([&](auto u) {
-        static_for<RM>([&](auto i) { static_for<RN>([&](auto j) { mma_i8(acc[i][j], fb[u][j], fa[u][i]); }); });
-      });
+      if (works)
+        static_for<2>([&](auto u) {
+          static_for<RM>([&](auto i) { static_for<RN>([&](auto j) { mma_i8(acc[i][j], fb[u][j], fa[u][i]); }); });
+        });
       phase_end();
     }
     if (g == 0) phase_end();

@@ -119,9 +119,9 @@ Pick with_split(const gemm_int8_s& h, int variant, int64_t want) {
   return p;
 }
 
-// The variant (and, for one product, the split of k) with the least predicted time among those that
-// load rows at any byte, or that need 16-byte rows.
-Pick choose(const gemm_int8_s& h, bool any) {
+// The variant (and, for one product, the split of k, up to `most`) with the least predicted time among
+// those that load rows at any byte, or that need 16-byte rows.
+Pick choose(const gemm_int8_s& h, bool any, int most) {
   const gemm_int8_desc& d = h.d;
   Pick best = with_split(h, -1, 1);
   double least = 0.0;
@@ -130,7 +130,7 @@ Pick choose(const gemm_int8_s& h, bool any) {
     if ((v.any != 0) != any || !fits(h, v)) continue;
     for (int s = 1; s <= 16; s *= 2) {
       const bool forced = d.split_k > 0 || d.form != GEMM_INT8_SINGLE;
-      if (forced && s > 1) break;
+      if ((forced && s > 1) || s > most) break;
       if (s > 1 && s * 4 > up(d.K, kSB)) break;
       const int split = forced ? std::max(d.split_k, 1) : s;
       const double us = predict(h, v, split);
@@ -182,9 +182,11 @@ int gemm_int8_create(const gemm_int8_desc* desc, gemm_int8_t* out) {
   h.vec = d.lda % 16 == 0 && d.ldb % 16 == 0 && (!batch || d.a_stride_l % 16 == 0) &&
           (!(batch || rows) || d.b_stride_l % 16 == 0) && 257 * d.lda < (int64_t(1) << 31) &&
           257 * d.ldb < (int64_t(1) << 31);
-  h.any = choose(h, true);
-  h.pick = h.vec ? choose(h, false) : h.any;
-  if (h.pick.variant < 0) h.pick = h.any;
+  if (h.vec) h.pick = choose(h, false, 16);
+  // for bases off 16 bytes in a handle for 16-byte rows: no more slices than its workspace holds
+  const bool usual = h.vec && h.pick.variant >= 0;
+  h.any = choose(h, true, usual ? h.pick.split : 16);
+  if (!usual) h.pick = h.any;
   if (h.pick.variant < 0) return GEMM_ERR_INVALID_ARG;
   gemm_int8_s* p = new (std::nothrow) gemm_int8_s(h);
   if (!p) return GEMM_ERR_INVALID_ARG;
@@ -196,7 +198,7 @@ int gemm_int8_create(const gemm_int8_desc* desc, gemm_int8_t* out) {
 int gemm_int8_workspace_size(gemm_int8_t h, size_t* bytes) {
   if (!h || h->magic != kLive) return GEMM_ERR_BAD_HANDLE;
   if (!bytes) return GEMM_ERR_INVALID_ARG;
-  *bytes = std::max(plane_bytes(*h, h->pick), h->any.variant < 0 ? 0 : plane_bytes(*h, h->any));
+  *bytes = plane_bytes(*h, h->pick);     // (of which h->any needs no more)
   return GEMM_OK;
 }
 
