@@ -212,7 +212,9 @@ __device__ __forceinline__ int64_t row_span(int64_t rows, int64_t ld, int64_t K)
 // Any alignment: BM x BN tiles by 2 x 2 waves, chunks through registers (16-byte loads at any byte)
 // into two LDS buffers, the loads of a block issued a block ahead, one barrier a block.  The rows
 // are placed in LDS as in the tiled kernel below.  Loads of rows past M or N have clamped addresses;
-// their outputs are not stored.
+// their outputs are not stored.  4096 x 4096 x 4095 without padding 123 us (rows on 16 bytes: 56), 333 x
+// 4096 x 8191 45 (27), 16 x 4096 x 4095 in 8 slices 15 (7): a load's latency is hidden by one block
+// only, and the chunks cross registers.
 // ------------------------------------------------------------------------------------------
 template <int BM, int BN, class OT, int OCC>
 __global__ __launch_bounds__(256, OCC) void i8_any(const SParams p) {
@@ -303,6 +305,13 @@ __global__ __launch_bounds__(256, OCC) void i8_any(const SParams p) {
 // DMA, one barrier per block.  Rows are placed in LDS so that a lane's rows are neighbours and its
 // outputs contiguous (scaled_tile in scaled.h).  KH = 2, for few tiles: two halves of the waves take
 // the even and the odd blocks of k through rings of their own and join in LDS at the end.
+//
+// 333 x 4096 x 8192 26.5 us: 0.31 us for a block of 64 x 128, 744 cycles of which LDS moves 72 KiB in
+// 576; only 192 of 256 CUs have a tile.  64 experts of 8 rows, N 2048, K 2048: 53 us, 5.1 TB/s of
+// weights.  Tried in place of it: B's rows straight into registers, without LDS (42 us for the 333 rows: 16
+// lanes that load from 16 rows take 16 cycles for each load); waves of 128 x 64 with blocks of 64 along
+// k and two workgroups a CU (4096^3 70 us, the ping-pong kernel 56); 64 x 128 by two waves of 64 x 64 (68
+// us for the experts), 64 x 256 and 32 x 256 tiles (within 4 % either way).
 // ------------------------------------------------------------------------------------------
 template <int BM, int BN, int WM, int WN, int ST, class OT, int OCC, int KH>
 __global__ __launch_bounds__(KH * WM * WN * 64, OCC) void i8_tile(const SParams p) {
@@ -414,7 +423,8 @@ __global__ __launch_bounds__(KH * WM * WN * 64, OCC) void i8_tile(const SParams 
 // Streaming kernel for few rows (decode): the cost is reading B once.  A workgroup owns 16 NBW
 // columns and 16 RM rows; its WK waves take slices of k, each streaming its blocks of B (and the
 // L2-resident rows of A) through a private LDS ring of R blocks by DMA, with no barrier in the
-// loop.  The waves' sums meet in LDS.
+// loop.  The waves' sums meet in LDS.  16 x 16384 x 8192 takes 26.4 us, 5.1 TB/s of the 6.3 that a
+// kernel reaches that only reads; 1 x 4096 x 4096 5.9 us, most of it the launch and one chain of loads.
 // ------------------------------------------------------------------------------------------
 template <int RM, int NBW, int WK, int R, class OT, int OCC>
 __global__ __launch_bounds__(WK * 64, OCC) void i8_stream(const SParams p) {
@@ -515,6 +525,13 @@ __global__ __launch_bounds__(WK * 64, OCC) void i8_stream(const SParams p) {
 // KiB): each A half in two slots, B in three; the units and their waits are those of gemm_pp
 // (pingpong.h): group g issues A half 1 - g of block v + 1 + g and its half of B(v + 2) in its read
 // phase of block v, 8 instructions, and lets at most those 8 be in flight at the end of it.
+//
+// 8192^3 takes 383 to 404 us on several cards (2,720 to 2,870 TOP/s; the library's int8 product reached
+// 2,380): matrix units busy 77 % of the cycles at 1.78 GHz, the board's power limit.  Short products pay
+// for the first blocks and the stores, about 15 us a tile that nothing overlaps: experts prefill, 8190
+// rows over 32, 103 us at 43 % busy.  Preferring the computing wave lost 0.5 to 4 %.  A form whose
+// workgroups take several tiles, the next one's first blocks coming during the stores, needed more
+// registers than there are (40 to 280 spilled) and was not run.
 // ------------------------------------------------------------------------------------------
 template <class OT>
 __global__ __launch_bounds__(512, 1) void i8_pp(const SParams p) {

@@ -135,7 +135,7 @@ typedef struct quant_rows_args {
 /* Enqueue the quantisation on `stream`.  Errors: GEMM_ERR_INVALID_ARG (also a row of more than 2^24
  * values), GEMM_ERR_DTYPE_COMBO, GEMM_ERR_LAYOUT, GEMM_ERR_MISALIGNED, GEMM_ERR_ARCH, GEMM_ERR_HIP,
  * GEMM_ERR_LAUNCH.  rows == 0 is a valid empty problem, and so is cols == 0 (which writes the scale of
- * rows of zeros). */
+ * rows of zeros).  q and scale may not overlap x, gate or row_index. */
 int quant_rows(const quant_rows_args* args, void* stream);
 
 #ifdef __cplusplus

@@ -100,8 +100,9 @@ int balance_grad(const balance_grad_args* args, void* stream);
  *
  *   y(p, :) = x(order[p] / topk, :),  zeros where order[p] is outside [0, tokens * topk)
  *
- * Every one of the `rows` rows is written.  The result goes by order alone; slot lets a token be read
- * once for all its rows, and may be NULL.  Its gradient is route_combine without weights. */
+ * Every one of the `rows` rows is written; y may not overlap x.  The result goes by order alone; slot
+ * lets a token be read once for all its rows, and may be NULL.  Its gradient is route_combine without
+ * weights. */
 typedef struct gather_args {
   const void* x;              /* tokens x cols, row stride ldx                                      */
   int32_t type;               /* GEMM_F32, GEMM_F16 or GEMM_BF16, of x and y                        */
@@ -120,7 +121,7 @@ int route_gather(const gather_args* args, void* stream);
  *
  * in fp32, the terms one after the other, rounded once.  Assignments whose slot is outside [0, rows)
  * add nothing (their weight and no row is looked at); without weights every weight is 1, without add
- * the sum starts from 0.  out may be add, with the same stride. */
+ * the sum starts from 0.  out may be add, with the same stride; it may not overlap y. */
 typedef struct combine_args {
   const void* y;              /* rows x cols, row stride ldy                                        */
   int32_t type;               /* of y, add and out                                                  */
