@@ -1,6 +1,6 @@
 // int8.h -- gfx950 kernels of the products in 8-bit integers (htint8.h).
 //
-//   D(m, n) = act(alpha * ((sum_k A(m, k) B(n, k)) * sA(m)) * sB(n) + beta C(m, n) + bias[n])
+//   D(m, n) = act(((sum_k A(m, k) B(n, k)) * (alpha sA(m))) * sB(n) + beta C(m, n) + bias[n])
 //
 // The sum is one 32-bit integer accumulator, fed by v_mfma_i32_16x16x64_i8 (16 cycles of a SIMD's
 // matrix unit, the rate of the 8-bit floats), and exact: slices and orders of k give the same bits,
@@ -54,8 +54,8 @@ __device__ __forceinline__ float scaled_sum(int sum, float sa, float sb) { retur
 // Outputs.  A lane has RM rows and in each RN pieces of 4 columns, dealt as Cols says, so that VO
 // outputs are 16 bytes of D, loaded (C) and stored as one piece at any alignment (the memory system
 // splits those that cross a line).  Waves whose columns all lie below N have a straight copy of the
-// code for each activation and for C or none; in the others (EDGE) a piece that N cuts goes element by
-// element.  Nothing but C is loaded between the stores: a wave waits for its stores before it sees a
+// code for each activation (with C, for none and for any), with D's rows on whole lines and without;
+// in the others (EDGE) a piece that N cuts goes element by element.  Nothing but C is loaded between the stores: a wave waits for its stores before it sees a
 // later load (an edge path that took row blocks through LDS cost the 6 workgroups of the last columns
 // 6 us: 333 x 4064 x 8192 31.9 us in place of 25.7).  With k in slices the integer sums go to the
 // slice's plane.
@@ -108,12 +108,26 @@ template <class OT, int RM, int RN> struct Finish {
   }
 };
 
-template <class OT, int RM, int RN, int ACT, bool HAS_C, bool EDGE, class RowOf>
+// Whole lines of 128 bytes go past the caches: 8192^3 400 -> 392 us, experts prefill 114 -> 106, 4096 x 4096
+// x 128 13.6 -> 12.1; rows that lines do not fit do not: 4001^3 66 us, with streamed stores 70.  (With 64
+// bytes of 16 rows a store 4096 x 4096 x 128 took 14.4 us.)
+typedef u32x4 unaligned16 __attribute__((aligned(2)));
+template <bool LINES> __device__ __forceinline__ void store_line(void* to, const u32x4& w, bool live) {
+  if (!live) return;
+  if constexpr (LINES) __builtin_nontemporal_store(w, reinterpret_cast<unaligned16*>(to));
+  else *reinterpret_cast<unaligned16*>(to) = w;
+}
+
+template <class OT, int RM, int RN, int ACT, bool HAS_C, bool EDGE, bool LINES, class RowOf>
 __device__ __forceinline__ void store_pieces(const SParams& p, const STile& s, const i32x4 (&acc)[RM][RN],
                                              const Finish<OT, RM, RN>& f, RowOf row_of, int64_t col, int x) {
   typedef Finish<OT, RM, RN> F;
   typedef Cols<OT> CM;
   constexpr int VO = F::VO, NQ = F::NQ, RG = RM % 2 == 0 ? 2 : 1;
+  // once for all rows, and not where they are loaded: that would be a wait before the loop
+  float sa[RM], bias[NQ][VO];
+  static_for<RM>([&](auto i) { sa[i] = f.sa[i] * p.alpha; });
+  static_for<NQ>([&](auto q) { static_for<VO>([&](auto e) { bias[q][e] = SOut<OT>::load(&f.bias[q], e); }); });
   // RG row blocks at a time, whose C is loaded before they are stored: D may be C, and more in hand at
   // once would not fit the registers
   static_for<RM / RG>([&](auto i0) {
@@ -128,28 +142,53 @@ __device__ __forceinline__ void store_pieces(const SParams& p, const STile& s, c
     });
     static_for<RG>([&](auto h) {
       constexpr int i = i0 * RG + h;
-      const int64_t row = row_of(i, x);
-      if (row < s.M) {
-        OT* d = (OT*)s.D + row * p.ldd + col;
-        static_for<NQ>([&](auto q) {
-          alignas(16) OT o[VO];
-          static_for<VO>([&](auto e) {
-            constexpr int j = q * CM::JP + e / 4, r = e % 4;
-            float y = scaled_sum(acc[i][j][r], f.sa[i], f.sb[j][r]) * p.alpha;
-            if constexpr (HAS_C) y += p.beta * SOut<OT>::load(&c[h][q], e);
-            y += SOut<OT>::load(&f.bias[q], e);
-            o[e] = SOut<OT>::bits(ACT < 0 ? activate(p.act, y) : ACT == 1 ? relu(y) : ACT == 2 ? gelu(y) : ACT == 3 ? silu(y) : y);
-          });
-          OT* to = d + CM::of(q * CM::JP, 0);
-          const int left = EDGE ? F::left(p, col, q) : VO;
-          if (!EDGE || left == VO) {
-            __builtin_memcpy(to, o, 16);
-          } else {
-            static_for<VO>([&](auto e) {
-              if (e < left) to[(int)e] = o[e];
-            });
-          }
+      auto form = [&](auto q, OT (&o)[VO]) {
+        static_for<VO>([&](auto e) {
+          constexpr int j = q * CM::JP + e / 4, r = e % 4;
+          float y = scaled_sum(acc[i][j][r], sa[i], f.sb[j][r]);
+          if constexpr (HAS_C) y += p.beta * SOut<OT>::load(&c[h][q], e);
+          y += bias[q][e];
+          o[e] = SOut<OT>::bits(ACT < 0 ? activate(p.act, y) : ACT == 1 ? relu(y) : ACT == 2 ? gelu(y) : ACT == 3 ? silu(y) : y);
         });
+      };
+      if constexpr (!EDGE && NQ % 2 == 0) {
+        // lanes x and x ^ 1 swap pieces, so that a store has 8 lanes on the even one's row and its 128
+        // bytes, and the next store the odd one's
+        const bool odd = x & 1;
+        const int64_t even_row = row_of(i, x & ~1), odd_row = row_of(i, x | 1);
+        static_for<NQ / 2>([&](auto half) {
+          constexpr int q = 2 * half;
+          alignas(16) OT o[2][VO];
+          form(std::integral_constant<int, q>{}, o[0]);
+          form(std::integral_constant<int, q + 1>{}, o[1]);
+          u32x4 w[2], theirs;
+          __builtin_memcpy(w, o, 32);
+          static_for<4>([&](auto d) {
+            const u32 give = odd ? w[0][(int)d] : w[1][(int)d];
+            theirs[(int)d] = (u32)__builtin_amdgcn_update_dpp(0, (int)give, 0xb1, 0xf, 0xf, true);  // quad_perm:[1,0,3,2]
+          });
+          OT* to = (OT*)s.D + col + (odd ? CM::of((q + 1) * CM::JP, 0) : CM::of(q * CM::JP, 0));
+          store_line<LINES>(to + even_row * p.ldd, odd ? theirs : w[0], even_row < s.M);
+          store_line<LINES>(to + odd_row * p.ldd, odd ? w[1] : theirs, odd_row < s.M);
+        });
+      } else {
+        const int64_t row = row_of(i, x);
+        if (row < s.M) {
+          OT* d = (OT*)s.D + row * p.ldd + col;
+          static_for<NQ>([&](auto q) {
+            alignas(16) OT o[VO];
+            form(q, o);
+            OT* to = d + CM::of(q * CM::JP, 0);
+            const int left = EDGE ? F::left(p, col, q) : VO;
+            if (!EDGE || left == VO) {
+              __builtin_memcpy(to, o, 16);
+            } else {
+              static_for<VO>([&](auto e) {
+                if (e < left) to[(int)e] = o[e];
+              });
+            }
+          });
+        }
       }
     });
   });
@@ -181,24 +220,37 @@ __device__ __forceinline__ void store_sums(const SParams& p, const STile& s, con
     return;
   }
   const int64_t col = col0 + CM::of(0, c4);
-  auto go = [&](auto act, auto edge) {
-    constexpr int A = decltype(act)::value;
-    constexpr bool E = decltype(edge)::value;
-    if (s.C) store_pieces<OT, RM, RN, A, true, E>(p, s, acc, f, row_of, col, x);
-    else store_pieces<OT, RM, RN, A, false, E>(p, s, acc, f, row_of, col, x);
+  auto go = [&](auto act, auto with_c, auto edge, auto lines) {
+    store_pieces<OT, RM, RN, decltype(act)::value, decltype(with_c)::value, decltype(edge)::value, decltype(lines)::value>(
+        p, s, acc, f, row_of, col, x);
   };
-  if (col0 + 16 * RN > p.N) go(std::integral_constant<int, -1>{}, std::true_type{});
-  else if (p.act == 0) go(std::integral_constant<int, 0>{}, std::false_type{});
-  else if (p.act == 3) go(std::integral_constant<int, 3>{}, std::false_type{});
-  else if (p.act == 2) go(std::integral_constant<int, 2>{}, std::false_type{});
-  else go(std::integral_constant<int, 1>{}, std::false_type{});
+  constexpr std::integral_constant<int, -1> any_act{};
+  constexpr std::integral_constant<int, 0> no_act{};
+  constexpr std::true_type yes{};
+  constexpr std::false_type no{};
+  if (col0 + 16 * RN > p.N) {
+    if (s.C) go(any_act, yes, yes, no);
+    else go(any_act, no, yes, no);
+    return;
+  }
+  auto whole = [&](auto lines) {
+    if (s.C) {
+      if (p.act == 0) go(no_act, yes, no, lines);
+      else go(any_act, yes, no, lines);
+    } else if (p.act == 0) go(no_act, no, no, lines);
+    else if (p.act == 3) go(std::integral_constant<int, 3>{}, no, no, lines);
+    else if (p.act == 2) go(std::integral_constant<int, 2>{}, no, no, lines);
+    else go(std::integral_constant<int, 1>{}, no, no, lines);
+  };
+  if (((reinterpret_cast<uintptr_t>(s.D) | (uintptr_t)(p.ldd * (int64_t)sizeof(OT))) & 127) == 0) whole(yes);
+  else whole(no);
 }
 
 // One output from its sum, its scales and its bias.
 template <class OT>
 __device__ __forceinline__ void finish_int(const SParams& p, const STile& s, int64_t row, int64_t col, int sum, float sa,
                                            float sb, float bias) {
-  float v = scaled_sum(sum, sa, sb) * p.alpha;
+  float v = scaled_sum(sum, sa * p.alpha, sb);
   if (s.C) v += p.beta * SOut<OT>::load(s.C, row * p.ldc + col);
   ((OT*)s.D)[row * p.ldd + col] = SOut<OT>::bits(activate(p.act, v + bias));
 }
@@ -528,8 +580,8 @@ __global__ __launch_bounds__(WK * 64, OCC) void i8_stream(const SParams p) {
 //
 // 8192^3 takes 383 to 404 us on several cards (2,720 to 2,870 TOP/s; the library's int8 product reached
 // 2,380): matrix units busy 77 % of the cycles at 1.78 GHz, the board's power limit.  Short products pay
-// for the first blocks and the stores, about 15 us a tile that nothing overlaps: experts prefill, 8190
-// rows over 32, 103 us at 43 % busy.  Preferring the computing wave lost 0.5 to 4 %.  A form whose
+// for the first blocks and the stores, which nothing overlaps (4096 x 4096 x 128, one block, 12.1 us, 7 of
+// them the outputs): experts prefill, 8190 rows over 32, 97 to 101 us at 43 % busy.  Preferring the computing wave lost 0.5 to 4 %.  A form whose
 // workgroups take several tiles, the next one's first blocks coming during the stores, needed more
 // registers than there are (40 to 280 spilled) and was not run.
 // ------------------------------------------------------------------------------------------

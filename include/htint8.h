@@ -2,7 +2,7 @@
  * htint8.h -- C ABI of the products in 8-bit integers with a scale for each token and each channel,
  * and of the quantisation that feeds them.
  *
- *   D = act( alpha * ((S(m, n) * a_scale[m]) * b_scale[n])  +  beta * C  +  bias[n] )
+ *   D = act( (S(m, n) * (alpha * a_scale[m])) * b_scale[n]  +  beta * C  +  bias[n] )
  *   S(m, n) = sum over k of A(m, k) * B(n, k)
  *
  * A and B hold signed 8-bit codes; S is exact (32-bit integers, K <= GEMM_INT8_MAX_K) and is rounded
