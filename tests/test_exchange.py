@@ -8,7 +8,8 @@ from int8_util import HALF, I32, LEAST, TYPE, gen, pitched, routing
 pytestmark = pytest.mark.gpu
 
 SIZES = [(1, 4, 1, 1, 1), (1, 8, 8, 8, 64), (5, 6, 3, 4, 7), (33, 5, 2, 16, 51), (40, 16, 7, 1, 512), (17, 12, 6, 3, 1000),
-         (70, 9, 8, 8, 2051), (3, 64, 9, 2, 4096), (12, 70, 64, 1, 130), (9, 20, 15, 5, 5003)]
+         (70, 9, 8, 8, 2051), (3, 64, 9, 2, 4096), (12, 70, 64, 1, 130), (9, 20, 15, 5, 5003), (257, 6, 5, 4, 16),
+         (300, 5, 2, 1, 17), (270, 9, 7, 1, 515), (260, 4, 3, 8, 2056), (1100, 3, 1, 1, 40)]
 DTYPES = ["bf16", "f16", "f32"]
 
 
