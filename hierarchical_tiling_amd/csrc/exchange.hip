@@ -72,7 +72,10 @@ template <int VE> struct Piece {
 // Rows are not kept in the caches: what is stored, and the rows that combine and its gradient read.
 // Stores that stay in an L2 are written back when the kernel ends, rows scattered over 1.1 GB at half the
 // rate: gather 217 us with streamed stores, 381 without (16384 tokens of 4096 to 8 of 256), and 16
-// tokens there and back 12.2 and 19.1 us; no size from 1 MB to 1 GB was better without.
+// tokens there and back 12.2 and 19.1 us; no size from 1 MB to 1 GB was better without.  So with rows on 16
+// bytes.  Of other rows a line is stored in two parts, which meet in an L2 only if they stay there: gather
+// does not stream them (8192 tokens of 4099 bf16 to 8: 137 us, streamed 162; of 2050 62 and 83; 16384 of
+// 4098 to 2, alone in losing, 83 and 71).  The gradient loses by it as often as it gains, and streams.
 typedef u32x4 piece_t __attribute__((aligned(2)));
 template <class T, int VE, bool STREAM = false>
 __device__ __forceinline__ void load_piece(const T* row, const Piece<VE>& q, T (&e)[VE]) {
@@ -87,12 +90,13 @@ __device__ __forceinline__ void load_piece(const T* row, const Piece<VE>& q, T (
 }
 // OVERLAP: the piece that the row's end cuts is stored whole, its first elements a second time with the
 // same values; not where they may have been read before (out that is add).
-template <class T, int VE, bool OVERLAP = false>
+template <class T, int VE, bool OVERLAP = false, bool STREAM = true>
 __device__ __forceinline__ void store_piece(T* row, const Piece<VE>& q, const T (&e)[VE]) {
   if ((OVERLAP || q.first == 0) && q.n == VE) {
     u32x4 w;
     __builtin_memcpy(&w, e, 16);
-    __builtin_nontemporal_store(w, reinterpret_cast<piece_t*>(row + q.at));
+    if constexpr (STREAM) __builtin_nontemporal_store(w, reinterpret_cast<piece_t*>(row + q.at));
+    else *reinterpret_cast<piece_t*>(row + q.at) = w;
   } else {
     static_for<VE>([&](auto i) {
       if (i >= q.first && i < q.n) __builtin_nontemporal_store(e[i], row + q.at + i);
@@ -142,8 +146,8 @@ template <class T> __device__ __forceinline__ const T* row_at(const void* base, 
 }
 
 // ---- gather --------------------------------------------------------------------------------
-// Elements are moved, not looked at: XT is DT_F32 or a 16-bit type.
-template <int XT>
+// Elements are moved, not looked at: XT is DT_F32 or a 16-bit type.  STREAM: y's rows lie on 16 bytes.
+template <int XT, bool STREAM>
 __global__ __launch_bounds__(1024) void gather_rows(const XParams p, int tpt) {
   typedef typename El<XT>::T T;
   constexpr int VE = El<XT>::VE, U = 2;
@@ -156,7 +160,7 @@ __global__ __launch_bounds__(1024) void gather_rows(const XParams p, int tpt) {
         const Piece<VE> q(c, p.cols);
         alignas(16) T e[VE];
         load_piece<T, VE>(x, q, e);
-        store_piece<T, VE, true>(y, q, e);
+        store_piece<T, VE, true, STREAM>(y, q, e);
       }
     });
     return;
@@ -183,7 +187,7 @@ __global__ __launch_bounds__(1024) void gather_rows(const XParams p, int tpt) {
       T* y = (T*)p.y + (int64_t)__builtin_amdgcn_readlane(s, __ffsll(todo) - 1) * p.ldy;
       static_for<U>([&](auto u) {
         const int c = c0 + (u * tpt + tid) * VE;
-        if (c < p.cols) store_piece<T, VE, true>(y, Piece<VE>(c, p.cols), e[u]);
+        if (c < p.cols) store_piece<T, VE, true, STREAM>(y, Piece<VE>(c, p.cols), e[u]);
       });
     }
   }
@@ -433,8 +437,13 @@ int route_gather(const gather_args* a, void* stream) {
   p.row_group = h.row_group;
   const dim3 grid((unsigned)(p.token_blocks + h.row_blocks)), block(h.threads);
   hipStream_t s = (hipStream_t)stream;
-  if (a->type == GEMM_F32) hipLaunchKernelGGL(gather_rows<DT_F32>, grid, block, 0, s, p, h.tpt);
-  else hipLaunchKernelGGL(gather_rows<DT_BF16>, grid, block, 0, s, p, h.tpt);
+  auto go = [&](auto xt) {
+    constexpr int XT = decltype(xt)::value;
+    if (on(a->y, 16) && a->ldy * size % 16 == 0) hipLaunchKernelGGL((gather_rows<XT, true>), grid, block, 0, s, p, h.tpt);
+    else hipLaunchKernelGGL((gather_rows<XT, false>), grid, block, 0, s, p, h.tpt);
+  };
+  if (a->type == GEMM_F32) go(std::integral_constant<int, DT_F32>{});
+  else go(std::integral_constant<int, DT_BF16>{});
   return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
