@@ -47,8 +47,15 @@ __device__ __forceinline__ u32x4 load16(const void* p) {
   return w;
 }
 
-// An output's sum as the float the epilogue goes on with.
-__device__ __forceinline__ float scaled_sum(int sum, float sa, float sb) { return ((float)sum * sa) * sb; }
+// One output before its activation; sa is alpha times A's scale.  Every kernel takes these steps with
+// these roundings, so that an output's bits do not depend on which it is: left to the compiler, some
+// rounded the product with sb before the bias was added to it, and others did not.
+template <bool HAS_C>
+__device__ __forceinline__ float scaled_sum(int sum, float sa, float sb, float beta, float c, float bias) {
+#pragma clang fp contract(off)
+  const float t = (float)sum * sa;
+  return HAS_C ? __builtin_fmaf(beta, c, t * sb) + bias : __builtin_fmaf(t, sb, bias);
+}
 
 // ------------------------------------------------------------------------------------------
 // Outputs.  A lane has RM rows and in each RN pieces of 4 columns, dealt as Cols says, so that VO
@@ -145,9 +152,8 @@ __device__ __forceinline__ void store_pieces(const SParams& p, const STile& s, c
       auto form = [&](auto q, OT (&o)[VO]) {
         static_for<VO>([&](auto e) {
           constexpr int j = q * CM::JP + e / 4, r = e % 4;
-          float y = scaled_sum(acc[i][j][r], sa[i], f.sb[j][r]);
-          if constexpr (HAS_C) y += p.beta * SOut<OT>::load(&c[h][q], e);
-          y += bias[q][e];
+          const float y = scaled_sum<HAS_C>(acc[i][j][r], sa[i], f.sb[j][r], p.beta, HAS_C ? SOut<OT>::load(&c[h][q], e) : 0.f,
+                                            bias[q][e]);
           o[e] = SOut<OT>::bits(ACT < 0 ? activate(p.act, y) : ACT == 1 ? relu(y) : ACT == 2 ? gelu(y) : ACT == 3 ? silu(y) : y);
         });
       };
@@ -250,9 +256,10 @@ __device__ __forceinline__ void store_sums(const SParams& p, const STile& s, con
 template <class OT>
 __device__ __forceinline__ void finish_int(const SParams& p, const STile& s, int64_t row, int64_t col, int sum, float sa,
                                            float sb, float bias) {
-  float v = scaled_sum(sum, sa * p.alpha, sb);
-  if (s.C) v += p.beta * SOut<OT>::load(s.C, row * p.ldc + col);
-  ((OT*)s.D)[row * p.ldd + col] = SOut<OT>::bits(activate(p.act, v + bias));
+  const float sa_alpha = sa * p.alpha;
+  const float v = s.C ? scaled_sum<true>(sum, sa_alpha, sb, p.beta, SOut<OT>::load(s.C, row * p.ldc + col), bias)
+                      : scaled_sum<false>(sum, sa_alpha, sb, 0.f, 0.f, bias);
+  ((OT*)s.D)[row * p.ldd + col] = SOut<OT>::bits(activate(p.act, v));
 }
 
 // Spans of a tile's rows for the range checks: up to the end of the chunk that K ends in.
