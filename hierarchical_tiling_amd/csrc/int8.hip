@@ -261,7 +261,7 @@ int gemm_int8_run(gemm_int8_t h, const gemm_int8_args* a, void* stream) {
   p.d_l = d.d_stride_l;
   p.as_l = d.a_scale_l;
   p.bs_l = d.b_scale_l;
-  p.alpha = a->alpha;
+  p.alpha = d.K > 0 ? a->alpha : 0.f;     // without k no alpha, were it infinite, reaches D
   p.beta = a->beta;
   p.act = d.act;
   p.form = d.form == GEMM_INT8_ROWS ? FORM_ROWS : d.form == GEMM_INT8_BATCH ? FORM_BATCH : FORM_SINGLE;
