@@ -222,7 +222,7 @@ int gemm_int8_run(gemm_int8_t h, const gemm_int8_args* a, void* stream) {
   if (!a) return GEMM_ERR_INVALID_ARG;
   const gemm_int8_desc& d = h->d;
   if ((d.form == GEMM_INT8_ROWS) != (a->offsets != nullptr)) return GEMM_ERR_INVALID_ARG;
-  if ((d.has_bias != 0) != (a->bias != nullptr)) return GEMM_ERR_INVALID_ARG;
+  if (d.has_bias ? !a->bias && d.N > 0 : a->bias != nullptr) return GEMM_ERR_INVALID_ARG;
   if (!d.has_c && a->beta != 0.0f) return GEMM_ERR_INVALID_ARG;
   const bool read_c = d.has_c && a->beta != 0.0f;
   const size_t osz = out_size(d.d_type);

@@ -70,7 +70,7 @@ typedef struct gemm_int8_args {
   const float* b_scale;       /* N values                                                          */
   const void* C;              /* read only when beta != 0                                          */
   void* D;
-  const void* bias;           /* N values, non-NULL iff has_bias                                   */
+  const void* bias;           /* N values; NULL without has_bias (and, without N, with it)         */
   const int32_t* offsets;     /* batch + 1 device values for GEMM_INT8_ROWS, else NULL             */
   float alpha, beta;
   void* workspace;            /* gemm_int8_workspace_size bytes, 16-byte aligned                   */
