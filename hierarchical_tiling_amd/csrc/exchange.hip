@@ -502,7 +502,7 @@ int route_combine_grad(const combine_grad_args* a, void* stream) {
   const bool dy = a->d_y && a->rows > 0 && a->cols > 0, dw = a->d_weights && a->tokens > 0;
   if (dy && (!a->order || (a->tokens > 0 && (!a->slot || !a->weights || !a->d_out)))) return GEMM_ERR_INVALID_ARG;
   if (dw && (!a->slot || (a->cols > 0 && (!a->d_out || (a->rows > 0 && !a->y))))) return GEMM_ERR_INVALID_ARG;
-  if (!a->d_y && !a->d_weights && a->tokens > 0 && a->rows > 0) return GEMM_ERR_INVALID_ARG;
+  if (!a->d_y && !a->d_weights && a->tokens > 0 && a->rows > 0 && a->cols > 0) return GEMM_ERR_INVALID_ARG;
   rc = arch_status();
   if (rc) return rc;
   if (!dy && !dw) return GEMM_OK;
