@@ -58,6 +58,8 @@ _COMBINE_GRAD = struct.Struct("@2P2i5q4PqPi4x")
 assert _GATHER.size == ctypes.sizeof(gather_args) and _COMBINE.size == ctypes.sizeof(combine_args)
 assert _COMBINE_GRAD.size == ctypes.sizeof(combine_grad_args)
 
+MAX_TOPK = 64      # ROUTE_MAX_TOPK
+
 EXPORTED = ["route_workspace_size", "route_experts", "balance_loss", "balance_grad", "route_gather", "route_combine",
             "route_combine_grad"]
 _lib = None
@@ -199,26 +201,33 @@ def balance_grad(logits, counts, topk, live, d_loss, d_logits, mask=None, coef=1
         raise GemmError(rc, "balance_grad")
 
 
-def gather(x, order, slot, y, stream=None):
+def gather(x, order, slot, y, stream=None, topk=None):
     """route_gather: the tokens x (tokens, cols) to their experts' rows y (rows, cols), by route()'s
-    order (rows) and slot (tokens, topk); rows of no assignment become zeros.  The gradient with
-    respect to x is combine() of y's gradient without weights."""
+    order (rows) and slot (tokens, topk); rows of no assignment become zeros.  slot may be None, with
+    the number of assignments a token has as topk: the same rows, each token read once for every one.
+    The gradient with respect to x is combine() of y's gradient without weights."""
     if _i32t is None:
         _types()
     dev, stream = _here(stream)
-    if x.dim() != 2 or slot.dim() != 2:
+    if x.dim() != 2:
         raise _bad("gather")
-    (tokens, cols), (n, topk), rows = x.shape, slot.shape, order.numel()
-    if (order.dtype is not _i32t or slot.dtype is not _i32t or n != tokens or y.dtype is not x.dtype or
-            y.shape != (rows, cols) or not order.is_contiguous() or not slot.is_contiguous() or
-            x.get_device() != dev or order.get_device() != dev or slot.get_device() != dev or y.get_device() != dev):
+    (tokens, cols), rows, at = x.shape, order.numel(), 0
+    if slot is not None:
+        if (slot.dim() != 2 or slot.dtype is not _i32t or slot.shape[0] != tokens or not slot.is_contiguous() or
+                slot.get_device() != dev or topk not in (None, slot.shape[1])):
+            raise _bad("gather")
+        topk, at = slot.shape[1], slot.data_ptr()
+    elif topk.__class__ is not int or not 1 <= topk <= MAX_TOPK:
+        raise _bad("gather")
+    if (order.dtype is not _i32t or y.dtype is not x.dtype or y.shape != (rows, cols) or not order.is_contiguous() or
+            x.get_device() != dev or order.get_device() != dev or y.get_device() != dev):
         raise _bad("gather")
     ldx = cols if x.is_contiguous() else pitch(x, tokens, cols)
     ldy = cols if y.is_contiguous() else pitch(y, rows, cols)
     if ldx < 0 or ldy < 0:
         raise _bad("gather")
     rc = (_lib or lib()).route_gather(_GATHER.pack(x.data_ptr(), type_code(x), topk, tokens, cols, ldx, order.data_ptr(),
-                                                   slot.data_ptr(), y.data_ptr(), rows, ldy), stream)
+                                                   at, y.data_ptr(), rows, ldy), stream)
     if rc:
         raise GemmError(rc, "route_gather")
 
