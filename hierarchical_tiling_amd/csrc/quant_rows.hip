@@ -202,11 +202,16 @@ template <int XT, bool GATE, bool STREAM> hipError_t launch(const QRParams& p, h
   else go(rows_to_int8<XT, GATE, STREAM, 1024, 4, true>, 1024);
   return hipGetLastError();
 }
-// An input that no cache holds is read past the caches: 16384 x 8192 bf16 (268 MB) 70 -> 66 us, 16384 x
-// 4096 34.7 -> 33.3; 20000 x 2048 (82 MB, three in turn) 20.3 -> 22.6.
+// An input that no cache holds and whose rows are read once is read past the caches: 16384 x 8192 bf16 (256
+// MiB) 72 -> 69 us, 16384 x 4096 (128) 36.8 -> 34.9, 16384 x 2048 with a gate (128) 36.7 -> 34.0, 16384 x
+// 8192 f32 (512) 120 -> 114, 65536 x 2048 bf16 in another order (256) 80 -> 75; but 20000 x 2048 bf16 (78)
+// 22.9 -> 24.3, 8192 x 2048 with a gate (64) 17.0 -> 20.1, 4096 x 4096 f32 (64) 15.1 -> 17.5.  Rows that go to
+// several places come from the caches after the first time: 65536 rows from 16384 x 4096 bf16 (128) 119 with
+// them, 131 past them, 32768 from 16384 x 4096 f32 (256) 101 and 119, with a gate (bf16, 256) 109 and 118.
 constexpr int64_t kStreamBytes = int64_t(1) << 27;
 template <int XT> hipError_t launch_type(const QRParams& p, hipStream_t s) {
-  const bool big = p.x_rows * p.cols >= kStreamBytes / (XT == DT_F32 ? 4 : 2);
+  const int64_t each = (XT == DT_F32 ? 4 : 2) * (p.gate ? 2 : 1);
+  const bool big = p.rows <= p.x_rows && p.rows * p.cols >= kStreamBytes / each;
   if (p.gate) return big ? launch<XT, true, true>(p, s) : launch<XT, true, false>(p, s);
   return big ? launch<XT, false, true>(p, s) : launch<XT, false, false>(p, s);
 }
