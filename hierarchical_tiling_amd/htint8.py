@@ -105,13 +105,23 @@ def _extents(d):
             N if d.has_bias else 0, L + 1 if d.form == FORMS["rows"] else 0)
 
 
-def _address(t, kinds, n, dev):
+def _address(t, kinds, n, dev, rows, cols, ld):
     """Address of a tensor on device dev whose type is one of `kinds` and whose memory has n values
-    from the first on; an address (or None) as it is."""
+    from the first on; an address (or None) as it is.  The memory is read as rows of `cols` values, ld
+    apart: a matrix of these rows and columns, or a vector (rows = 1), that lies otherwise raises."""
     if t is None or t.__class__ is int:
         return t or 0
-    if t.get_device() != dev or t.dtype not in kinds or not (
-            (t.numel() >= n and t.is_contiguous()) or _bytes(t) >= n * t.element_size()):
+    whole = t.is_contiguous()
+    ok = t.get_device() == dev and t.dtype in kinds and (
+        (whole and t.numel() >= n) or _bytes(t) >= n * t.element_size())
+    if ok and n and rows > 1:
+        if t.dim() > 1 and t.shape[-1] == cols and t.shape[-2] == rows:
+            step, one = t.stride()[-2:]
+            ok = step == ld and (one == 1 or cols == 1)
+    elif ok and n and not whole and cols > 1:
+        # the innermost dimension that has several values
+        ok = next((step for size, step in zip(reversed(t.shape), reversed(t.stride())) if size > 1), 1) == 1
+    if not ok:
         raise GemmError(GEMM_ERR_INVALID_ARG, "gemm_int8_run")
     return t.data_ptr()
 
@@ -124,9 +134,10 @@ class Int8Gemm:
     """RAII wrapper: a handle for one product's description.
 
     run() raises GemmError for tensors on another device than the current one, of another type than
-    the description's (codes: int8), or whose memory ends before the product's does, and for a
-    workspace of fewer than workspace_bytes.  Device addresses are taken as they are.  C is looked at
-    only when beta is not 0."""
+    the description's (codes: int8), or whose memory ends before the product's does, for matrices of the
+    product's rows and columns whose strides are not the description's, for scales, bias and offsets
+    whose values are not neighbours, and for a workspace of fewer than workspace_bytes.  Device
+    addresses are taken as they are.  C is looked at only when beta is not 0."""
 
     def __init__(self, desc: gemm_int8_desc):
         self.handle = None
@@ -170,12 +181,16 @@ class Int8Gemm:
         if usual:
             A, a_scale, B, b_scale, D = A.data_ptr(), a_scale.data_ptr(), B.data_ptr(), b_scale.data_ptr(), D.data_ptr()
         else:
-            A, a_scale = _address(A, codes, nA, dev), _address(a_scale, f32, nSA, dev)
-            B, b_scale = _address(B, codes, nB, dev), _address(b_scale, f32, nSB, dev)
-            D = _address(D, out, nD, dev)
-        C = 0 if C is None or not beta else _address(C, out, nC, dev)
-        bias = 0 if bias is None else _address(bias, out, n_bias, dev)
-        offsets = 0 if offsets is None else _address(offsets, i32, n_offsets, dev)
+            d = self.desc
+            A, a_scale = _address(A, codes, nA, dev, d.M, d.K, d.lda), _address(a_scale, f32, nSA, dev, 1, d.M, 0)
+            B, b_scale = _address(B, codes, nB, dev, d.N, d.K, d.ldb), _address(b_scale, f32, nSB, dev, 1, d.N, 0)
+            D = _address(D, out, nD, dev, d.M, d.N, d.ldd)
+        if C is None or not beta:
+            C = 0
+        else:
+            C = _address(C, out, nC, dev, self.desc.M, self.desc.N, self.desc.ldc)
+        bias = 0 if bias is None else _address(bias, out, n_bias, dev, 1, n_bias, 0)
+        offsets = 0 if offsets is None else _address(offsets, i32, n_offsets, dev, 1, n_offsets, 0)
         if workspace is None:
             workspace = 0
         elif workspace.__class__ is not int:
