@@ -3,8 +3,9 @@
 //   D(m, n) = act(((sum_k A(m, k) B(n, k)) * (alpha sA(m))) * sB(n) + beta C(m, n) + bias[n])
 //
 // The sum is one 32-bit integer accumulator, fed by v_mfma_i32_16x16x64_i8 (16 cycles of a SIMD's
-// matrix unit, the rate of the 8-bit floats), and exact: slices and orders of k give the same bits,
-// and nothing but matrix instructions and fragment reads stands in the loop over k.
+// matrix unit, the rate of the 8-bit floats), and exact: slices and orders of k give the same bits (and
+// so does every kernel, as all take the steps behind the sum alike, scaled_sum), and nothing but matrix
+// instructions and fragment reads stands in the loop over k.
 //
 // Operands are swapped in the instruction, as in scaled.h: B's rows (n) are its A operand and A's
 // rows (m) its B operand, so that a lane's four accumulators are four neighbouring n of one m.
@@ -62,10 +63,10 @@ __device__ __forceinline__ float scaled_sum(int sum, float sa, float sb, float b
 // outputs are 16 bytes of D, loaded (C) and stored as one piece at any alignment (the memory system
 // splits those that cross a line).  Waves whose columns all lie below N have a straight copy of the
 // code for each activation (with C, for none and for any), with D's rows on whole lines and without;
-// in the others (EDGE) a piece that N cuts goes element by element.  Nothing but C is loaded between the stores: a wave waits for its stores before it sees a
-// later load (an edge path that took row blocks through LDS cost the 6 workgroups of the last columns
-// 6 us: 333 x 4064 x 8192 31.9 us in place of 25.7).  With k in slices the integer sums go to the
-// slice's plane.
+// in the others (EDGE) a piece that N cuts goes element by element.  Nothing but C is loaded between
+// the stores: a wave waits for its stores before it sees a later load (an edge path that took row
+// blocks through LDS cost the 6 workgroups of the last columns 6 us: 333 x 4064 x 8192 31.9 us in place
+// of 25.7).  With k in slices the integer sums go to the slice's plane.
 // ------------------------------------------------------------------------------------------
 // What a lane's outputs need besides their sums and C: scales of its rows and columns, and the bias of
 // its pieces.  Kernels with registers to spare load it before their loop, so that a short product
@@ -83,7 +84,8 @@ template <class OT, int RM, int RN> struct Finish {
   }
   // 16 bytes of piece q of a row, zeros past N.
   template <bool EDGE>
-  __device__ static __forceinline__ u32x4 piece(const SParams& p, const void* base, int64_t row, int64_t ld, int64_t col, int q) {
+  __device__ static __forceinline__ u32x4 piece(const SParams& p, const void* base, int64_t row, int64_t ld, int64_t col,
+                                                int q) {
     const OT* src = (const OT*)base + row * ld + col + CM::of(q * CM::JP, 0);
     if (!EDGE || left(p, col, q) == VO) return load16(src);
     alignas(16) OT e[VO];
@@ -110,14 +112,17 @@ template <class OT, int RM, int RN> struct Finish {
     }
     if (p.bias) {
       const int64_t col = col0 + CM::of(0, c4);
-      static_for<NQ>([&](auto q) { bias[q] = whole ? piece<false>(p, p.bias, 0, 0, col, q) : piece<true>(p, p.bias, 0, 0, col, q); });
+      static_for<NQ>([&](auto q) {
+        bias[q] = whole ? piece<false>(p, p.bias, 0, 0, col, q) : piece<true>(p, p.bias, 0, 0, col, q);
+      });
     }
   }
 };
 
-// Whole lines of 128 bytes go past the caches: 8192^3 400 -> 392 us, experts prefill 114 -> 106, 4096 x 4096
-// x 128 13.6 -> 12.1; rows that lines do not fit do not: 4001^3 66 us, with streamed stores 70.  (With 64
-// bytes of 16 rows a store 4096 x 4096 x 128 took 14.4 us.)
+// Stores of whole lines of 128 bytes go past the caches: 4096 x 4096 x 128 13.0 -> 11.6 us, 2048^3 16.3 ->
+// 15.3, experts prefill 104 -> 101, 8192^3 403 -> 396 (a graph's runs, in turn).  Rows that lines do not fit
+// go through them: 4001^3 66 us, streamed 70.  (Without the exchange of pieces below, a store has 64 bytes
+// of 16 rows and none is streamed: 13.6, 16.1, 104 and 402.)
 typedef u32x4 unaligned16 __attribute__((aligned(2)));
 template <bool LINES> __device__ __forceinline__ void store_line(void* to, const u32x4& w, bool live) {
   if (!live) return;
@@ -152,9 +157,13 @@ __device__ __forceinline__ void store_pieces(const SParams& p, const STile& s, c
       auto form = [&](auto q, OT (&o)[VO]) {
         static_for<VO>([&](auto e) {
           constexpr int j = q * CM::JP + e / 4, r = e % 4;
-          const float y = scaled_sum<HAS_C>(acc[i][j][r], sa[i], f.sb[j][r], p.beta, HAS_C ? SOut<OT>::load(&c[h][q], e) : 0.f,
-                                            bias[q][e]);
-          o[e] = SOut<OT>::bits(ACT < 0 ? activate(p.act, y) : ACT == 1 ? relu(y) : ACT == 2 ? gelu(y) : ACT == 3 ? silu(y) : y);
+          const float y = scaled_sum<HAS_C>(acc[i][j][r], sa[i], f.sb[j][r], p.beta,
+                                            HAS_C ? SOut<OT>::load(&c[h][q], e) : 0.f, bias[q][e]);
+          o[e] = SOut<OT>::bits(ACT < 0    ? activate(p.act, y)
+                                : ACT == 1 ? relu(y)
+                                : ACT == 2 ? gelu(y)
+                                : ACT == 3 ? silu(y)
+                                           : y);
         });
       };
       if constexpr (!EDGE && NQ % 2 == 0) {
@@ -586,11 +595,12 @@ __global__ __launch_bounds__(WK * 64, OCC) void i8_stream(const SParams p) {
 // phase of block v, 8 instructions, and lets at most those 8 be in flight at the end of it.
 //
 // 8192^3 takes 383 to 404 us on several cards (2,720 to 2,870 TOP/s; the library's int8 product reached
-// 2,380): matrix units busy 77 % of the cycles at 1.78 GHz, the board's power limit.  Short products pay
-// for the first blocks and the stores, which nothing overlaps (4096 x 4096 x 128, one block, 12.1 us, 7 of
-// them the outputs): experts prefill, 8190 rows over 32, 97 to 101 us at 43 % busy.  Preferring the computing wave lost 0.5 to 4 %.  A form whose
-// workgroups take several tiles, the next one's first blocks coming during the stores, needed more
-// registers than there are (40 to 280 spilled) and was not run.
+// 2,380): matrix units busy 78 % of the cycles at 1.8 GHz, the board's power limit.  Short products pay
+// for the first blocks and the stores, which nothing overlaps (4096 x 4096 x 128, one block, 11.6 us, 7 of
+// them the outputs): experts prefill, 8190 rows over 32, 97 to 105 us at 44 % busy.  Preferring the
+// computing wave lost 0.5 to 4 %.  A form whose workgroups take several tiles, the next one's first blocks
+// coming during the stores, spilled 248 registers (39 with both groups working in every tile, none without
+// the epilogue, or with one tile) and was not run.
 // ------------------------------------------------------------------------------------------
 template <class OT>
 __global__ __launch_bounds__(512, 1) void i8_pp(const SParams p) {
@@ -751,10 +761,11 @@ template <class OT> hipError_t go_join(const SParams& p, dim3 grid, hipStream_t 
   return hipGetLastError();
 }
 template <class OT> const Int8Launches& int8_launches() {
-  static const Int8Launches table = {{&go_any<64, 128, OT, 2>, &go_any<128, 128, OT, 2>, &go_stream<1, 2, 4, 3, 2, OT>, &go_stream<1, 1, 8, 4, 1, OT>,
-           &go_stream<2, 2, 4, 3, 1, OT>, &go_stream<4, 2, 4, 3, 1, OT>, &go_tile<64, 128, 2, 2, 3, 2, 1, OT>,
-           &go_tile<64, 128, 2, 2, 3, 1, 2, OT>, &go_tile<128, 128, 2, 2, 2, 2, 1, OT>,
-           &go_tile<128, 128, 2, 2, 2, 1, 2, OT>, &go_pp<OT>, &go_join<OT>}};
+  static const Int8Launches table = {
+      {&go_any<64, 128, OT, 2>, &go_any<128, 128, OT, 2>, &go_stream<1, 2, 4, 3, 2, OT>, &go_stream<1, 1, 8, 4, 1, OT>,
+       &go_stream<2, 2, 4, 3, 1, OT>, &go_stream<4, 2, 4, 3, 1, OT>, &go_tile<64, 128, 2, 2, 3, 2, 1, OT>,
+       &go_tile<64, 128, 2, 2, 3, 1, 2, OT>, &go_tile<128, 128, 2, 2, 2, 2, 1, OT>,
+       &go_tile<128, 128, 2, 2, 2, 1, 2, OT>, &go_pp<OT>, &go_join<OT>}};
   return table;
 }
 

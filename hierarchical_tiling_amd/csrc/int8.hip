@@ -15,9 +15,10 @@ namespace {
 constexpr uint32_t kLive = 0x494e5438u, kDead = 0xdeadbeefu;
 constexpr int64_t kCUs = 256;
 
-// One kernel (of Int8Launches): its tile, whether it loads rows at any byte, and what choose() goes by: workgroups a CU holds at once (occ), waves (or halves of them) that share
-// k (kw), microseconds for a block of 128 of k while a CU has one workgroup (c1) and while it has occ
-// of them (c2), and for each round of workgroups beside them (round).  Measured on MI355X.
+// One kernel (of Int8Launches): its tile, whether it loads rows at any byte, and what choose() goes by:
+// workgroups a CU holds at once (occ), waves (or halves of them) that share k (kw), microseconds for a
+// block of 128 of k while a CU has one workgroup (c1) and while it has occ of them (c2), and for each
+// round of workgroups beside them (round).  Measured on MI355X.
 struct Cost {
   int occ, kw;
   float c1, c2, round;
@@ -90,8 +91,9 @@ double expected_row_tiles(const gemm_int8_s& h, int bm) {
 // block, against the time that the operands' bytes take at 6 TB/s (of the less of the two 0.41 counts:
 // they overlap in part), plus the second kernel of a split.  The costs are fitted to 132 products and
 // groups of rows (1 to 16384 rows, 512 to 14336 columns, k of 512 to 8192, 8 to 128 experts, each kernel
-// and slices of k forced in turn): the choice is on average 0.4 % above the fastest, 7 % at most (16384
-// rows over 128 experts); costs taken from single rounds alone gave 0.7 %.
+// and slices of k forced in turn), before stores went out in whole lines and a group of waves without rows
+// did no work: then the choice was on average 0.4 % above the fastest and 7 % at most, with the kernels as
+// they are 0.6 % and 17 % (16384 rows over 128 experts, 224 us for 191; the next 9 %, 3000 x 1024 x 8192).
 double predict(const gemm_int8_s& h, const Variant& v, int split) {
   const gemm_int8_desc& d = h.d;
   const Cost& c = v.cost;

@@ -3,7 +3,7 @@
 //   t = max(largest |x|, 127 * 2^-126),  scale = t / 127,  q = clamp(rint(x * (127 / t)), -127, 127)
 //
 // A row is read once and kept in registers between the maximum and the conversion.  Bound by
-// memory: 16384 x 8192 bf16 66 us, 6.1 TB/s (a copy reaches 4.7, a kernel that only reads 6.3).  Codes
+// memory: 16384 x 8192 bf16 66 us, 6.1 TB/s (a copy reaches 5.0, a kernel that only reads 6.3).  Codes
 // are stored past the caches (16384 x 8192 75 -> 70 us, 20000 x 2048 26 -> 20; small ones are alike).
 #include <algorithm>
 

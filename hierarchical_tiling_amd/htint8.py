@@ -253,7 +253,8 @@ def quantize(x, q, scale, gate=None, act=None, row_index=None, index_div=1, pad=
             ldg, at, code = pitch(gate, x_rows, cols), gate.data_ptr(), ACTS["silu" if act is None else act]
             ok = ldg >= 0
     ok = (ok and q.dtype is _i8 and scale.dtype is _f32t and q.shape == (rows, cols) and scale.numel() == rows and
-          0 < index_div < 1 << 31 and scale.is_contiguous() and x.get_device() == dev and q.get_device() == dev and scale.get_device() == dev)
+          0 < index_div < 1 << 31 and scale.is_contiguous() and x.get_device() == dev and q.get_device() == dev and
+          scale.get_device() == dev)
     if ok:
         step = cols if x.is_contiguous() else pitch(x, x_rows, cols)
         # (of one padded row the stride says how far its padding may go)

@@ -7,7 +7,7 @@
  *
  * A and B hold signed 8-bit codes; S is exact (32-bit integers, K <= GEMM_INT8_MAX_K) and is rounded
  * to fp32 once; the steps behind it are fp32, in the order above, with one rounding each at most; D
- * is rounded once more.  The result does not depend on how k is split.
+ * is rounded once more.  An output's bits depend neither on how k is split nor on the kernel.
  *
  * Status codes, element types and activations are those of htgemm.h.  The caller owns every
  * device buffer and the stream; calls are asynchronous; the buffers and the stream belong to the
