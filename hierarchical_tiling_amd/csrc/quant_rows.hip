@@ -185,6 +185,8 @@ dim3 grid_of(int64_t blocks) {
 // Threads for each row: a wave for short rows, a workgroup for longer ones, and more of them while there
 // are too few rows to fill the card (480 x 2048 with 256 threads a row 2.8 us, a wave 3.4, gated 3.6 and
 // 6.7; 4096 x 2048 6.5 and 6.0; 1 x 8192 with 1024 threads 2.6, 256 3.1; 2000 x 8192 10.8 and 9.4).
+// Few rows, and rows that are read twice, are not streamed (below).
+constexpr int kHeld = 1024 * 4 * 8;      // columns that a workgroup holds; rows of more are read twice
 template <int XT, bool GATE, bool STREAM> hipError_t launch(const QRParams& p, hipStream_t s) {
   auto go = [&](auto kernel, int tpr) {
     const int per = tpr < 256 ? 256 / tpr : 1;
@@ -192,14 +194,14 @@ template <int XT, bool GATE, bool STREAM> hipError_t launch(const QRParams& p, h
   };
   const int n = p.q_cols;
   if (n <= 512) go(rows_to_int8<XT, GATE, STREAM, 64, 1, false>, 64);
-  else if (n <= 2048 && p.rows <= 1024) go(rows_to_int8<XT, GATE, STREAM, 256, 1, false>, 256);
+  else if (n <= 2048 && p.rows <= 1024) go(rows_to_int8<XT, GATE, false, 256, 1, false>, 256);
   else if (n <= 1024) go(rows_to_int8<XT, GATE, STREAM, 64, 2, false>, 64);
   else if (n <= 2048) go(rows_to_int8<XT, GATE, STREAM, 64, 4, false>, 64);
   else if (n <= 4096) go(rows_to_int8<XT, GATE, STREAM, 256, 2, false>, 256);
-  else if (n <= 8192 && p.rows <= 256) go(rows_to_int8<XT, GATE, STREAM, 1024, 1, false>, 1024);
+  else if (n <= 8192 && p.rows <= 256) go(rows_to_int8<XT, GATE, false, 1024, 1, false>, 1024);
   else if (n <= 8192) go(rows_to_int8<XT, GATE, STREAM, 256, 4, false>, 256);
-  else if (n <= 32768) go(rows_to_int8<XT, GATE, STREAM, 1024, 4, false>, 1024);
-  else go(rows_to_int8<XT, GATE, STREAM, 1024, 4, true>, 1024);
+  else if (n <= kHeld) go(rows_to_int8<XT, GATE, STREAM, 1024, 4, false>, 1024);
+  else go(rows_to_int8<XT, GATE, false, 1024, 4, true>, 1024);
   return hipGetLastError();
 }
 // An input that no cache holds and whose rows are read once is read past the caches: 16384 x 8192 bf16 (256
@@ -207,11 +209,12 @@ template <int XT, bool GATE, bool STREAM> hipError_t launch(const QRParams& p, h
 // 8192 f32 (512) 120 -> 114, 65536 x 2048 bf16 in another order (256) 80 -> 75; but 20000 x 2048 bf16 (78)
 // 22.9 -> 24.3, 8192 x 2048 with a gate (64) 17.0 -> 20.1, 4096 x 4096 f32 (64) 15.1 -> 17.5.  Rows that go to
 // several places come from the caches after the first time: 65536 rows from 16384 x 4096 bf16 (128) 119 with
-// them, 131 past them, 32768 from 16384 x 4096 f32 (256) 101 and 119, with a gate (bf16, 256) 109 and 118.
+// them, 131 past them, 32768 from 16384 x 4096 f32 (256) 101 and 119, with a gate (bf16, 256) 109 and 118.  So do
+// rows that are read twice: 4000 x 40000 bf16 89 and 92, f32 148 and 173, 2000 x 65536 f32 138 and 168.
 constexpr int64_t kStreamBytes = int64_t(1) << 27;
 template <int XT> hipError_t launch_type(const QRParams& p, hipStream_t s) {
   const int64_t each = (XT == DT_F32 ? 4 : 2) * (p.gate ? 2 : 1);
-  const bool big = p.rows <= p.x_rows && p.rows * p.cols >= kStreamBytes / each;
+  const bool big = p.rows <= p.x_rows && p.q_cols <= kHeld && p.rows * p.cols >= kStreamBytes / each;
   if (p.gate) return big ? launch<XT, true, true>(p, s) : launch<XT, true, false>(p, s);
   return big ? launch<XT, false, true>(p, s) : launch<XT, false, false>(p, s);
 }
